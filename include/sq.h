@@ -20,6 +20,9 @@
  *     sq_w4a4_linear (+ _workspace_bytes, _tail_workspace_bytes, _noalloc).
  *   - KV path: sq_rope_tables, sq_kv_rotate_quant (RoPE + R3 + 4-bit caches),
  *     sq_kv_dequant, sq_kv4_decode_attention (+ _workspace_bytes).
+ *   - Paged KV path: sq_kv_paged_append, sq_kv_paged_dequant,
+ *     sq_kv_paged_attention, sq_kv_prefix_attention
+ *     (+ sq_kv_attention_workspace_bytes).
  *   - W4A8KV8 ("SpinQuant, Reproduced", Q7): sq_rotate_quant8,
  *     sq_w4a8_linear, sq_kv_rotate_quant8, sq_kv8_dequant,
  *     sq_kv8_decode_attention.
@@ -522,6 +525,153 @@ sq_status sq_kv8_decode_attention(const void* q, const uint8_t* k_cache, const f
                                   const int32_t* lengths, int64_t B, int64_t S_max, int hq,
                                   int hkv, int d, void* out, void* workspace,
                                   size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The paged KV cache: the 4- and 8-bit caches above in pages, for ragged
+ * batches of sequences that grow.
+ *
+ * Source: "SpinQuant, Reproduced", Q5 and Q7 (where R3 sits; 4- and 8-bit KV
+ * caches; the Qwen3-8B attention, whose queries and keys are normalised per
+ * head before the rotary embedding).  Pages, ragged batches and the score
+ * rules below are serving forms with no counterpart in the pages.
+ *
+ * A pool of pages, head-major: codes [num_pages][hkv][page_size][d * bits / 8]
+ * (packed as sq_kv_rotate_quant / sq_kv_rotate_quant8 pack them), scale
+ * (float32) and zero (uint8) [num_pages][hkv][page_size].  (Flattened to T =
+ * num_pages, h = hkv * page_size, a pool is what sq_kv_dequant reads.)
+ *
+ * A ragged batch of B sequences: their new tokens are packed, sequence b's
+ * being rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of T (cu_seqlens device
+ * int32 [B + 1], not decreasing, from 0 to at most T; rows behind the last
+ * sequence are left as they are).  Row p % page_size of page
+ * block_table[b][p / page_size] (device int32 [B][table_width]) holds position
+ * p of sequence b; entries that no position reaches are not read.
+ *
+ * Lengths, page numbers and positions live on the device and are checked
+ * there: what is out of range is reported through sq_device_status() as
+ * SQ_ERR_INVALID_ARG and nothing outside the arrays is read or written.
+ * The int32 arrays, slopes and lse need only 4-byte alignment.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  uint8_t* k_codes;
+  float* k_scale;
+  uint8_t* k_zero;
+  uint8_t* v_codes;
+  float* v_scale;
+  uint8_t* v_zero;
+  int64_t num_pages;
+  int page_size;                 /* a power of two, 16..4096 */
+  int hkv;                       /* 1..64 */
+  int d;                         /* 128 */
+  int bits;                      /* 4 or 8 */
+} sq_kv_pages;                   /* a HOST struct of device pointers, all 16-byte aligned */
+
+/* sq_kv_paged_append -- the new tokens of a ragged batch into the cache, and
+ * their rotated queries.
+ *
+ * Token i of sequence b gets position p = cached[b] + i.  Per head:
+ *   norm (where a weight is given):  x <- x * w / sqrt(mean(x^2) + eps)
+ *   rotary embedding of the first `rot` channels (where tables are given),
+ *   with c, s = rope_cos, rope_sin[p][j], j < rot / 2, for the pair (a, b) =
+ *   (x_j, x_{j + rot/2}), or (x_2j, x_{2j+1}) when interleaved:
+ *     a' = a c - b s,  b' = b c + a s
+ *   Q and K:  y = x . H_128 / sqrt(128) (Sylvester, natural order).
+ *   q_out = bf16(y_q);  y_k and the unrotated v go to their page with the
+ *   quantizer of sq_kv_rotate_quant (4 bits) or sq_kv_rotate_quant8 (8 bits).
+ *   Precision as sq_kv_rotate_quant: Q in float32, K in double precision
+ *   rounded once to float32, quotients exactly rounded.
+ *
+ * q, k, v    device bf16 [T][hq or hkv][d], heads contiguous, q_stride /
+ *            k_stride / v_stride elements between tokens (multiples of 8, so
+ *            slices of one fused projection serve); 16-byte aligned.
+ * cached     device int32 [B]: tokens already in the cache.
+ * rope_cos, rope_sin  device float32 [max_pos][rot / 2], or both NULL.
+ *            Positions from max_pos on are out of range.
+ * rot        rotated channels: a multiple of 16, 16..128 (read with tables).
+ * q_norm, k_norm  device float32 [d], or NULL.  eps >= 0.
+ * q_out      device bf16 [T][hq][d] (written; may not overlap q).
+ * A token whose sequence, position or page is out of range is reported and
+ * written nowhere.  The positions of one call must lie in different rows:
+ * of two tokens sent to the same row (a page in two sequences' tables at the
+ * place where both grow), which one's codes, scale and zero point it ends
+ * with is undefined.
+ * Shape rules: T >= 0, B >= 0, 1 <= hq <= 256, hq % hkv == 0. */
+sq_status sq_kv_paged_append(const void* q, const void* k, const void* v, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, int64_t T, int hq,
+                             const sq_kv_pages* pages, const int32_t* block_table,
+                             int table_width, const int32_t* cu_seqlens, const int32_t* cached,
+                             int B, const float* rope_cos, const float* rope_sin, int max_pos,
+                             int rot, int interleaved, const float* q_norm, const float* k_norm,
+                             float eps, void* q_out, void* stream);
+
+/* sq_kv_paged_dequant -- read-back: for the token at position cached[b] + i of
+ * sequence b, packed row t,
+ *     out[t][h][j] = bf16((code - zero) * scale)        (K and V, bf16 [T][hkv][d]).
+ * With cached = 0 and cu_seqlens the sequences' lengths it reads whole
+ * sequences.  Tokens out of range are reported and left unwritten. */
+sq_status sq_kv_paged_dequant(const sq_kv_pages* pages, const int32_t* block_table,
+                              int table_width, const int32_t* cu_seqlens, const int32_t* cached,
+                              int B, int64_t T, void* k_out, void* v_out, void* stream);
+
+/* How attention scores are formed.  For the query at position p and the key
+ * at position j <= p (later keys are hidden):
+ *     s = scale * (q . k_hat);  softcap > 0:  s = softcap * tanh(s / softcap);
+ *     slopes:  s -= slopes[head] * (p - j);  window > 0: keys with p - j >= window are hidden. */
+typedef struct {
+  float scale;                   /* finite; 1/sqrt(128) is usual */
+  float softcap;                 /* finite, 0: none */
+  int window;                    /* 0..2^30, 0: none */
+  const float* slopes;           /* device float32 [hq], or NULL */
+} sq_score_rule;
+
+/* sq_kv_paged_attention -- causal attention of the new tokens over their
+ * sequences' pages (which already hold them: append first).
+ *
+ * Token i of sequence b is at position p = lengths[b] - n_b + i, n_b its
+ * number of new tokens, and query head h reads KV head h / (hq / hkv):
+ *     out = sum_j softmax_j(s) v_hat_j,   lse = ln sum_j exp(s),
+ * over the visible j <= p.  Products with the codes are exact and sums are in
+ * float32; the output is rounded once to bf16.  A row with no visible key (p < 0) gets
+ * zeros and lse -inf.
+ *
+ * q          device bf16 [T][hq][d] (q_out of the append), heads contiguous,
+ *            q_stride elements between tokens (a multiple of 8).
+ * lengths    device int32 [B]: cached tokens, the new ones included.  A
+ *            sequence whose length is out of range (of its table) is reported
+ *            and gets zeros; one whose rows do not lie in the batch is
+ *            reported and left out.  Rows of a page that is out of range
+ *            are reported and taken as hidden.
+ * max_q      the most new tokens that any sequence has.  It picks the kernel:
+ *            results hold for longer sequences too, at a lower speed.
+ * out        device bf16 [T][hq][d];  lse  device float32 [T][hq], or NULL.
+ * workspace  device scratch of sq_kv_attention_workspace_bytes() bytes, zero
+ *            on first use and left zero where it must be by every call that
+ *            finishes; one call at a time per workspace.  With less (or NULL)
+ *            the keys of a row are not split across CTAs: the same result but
+ *            for the order of float32 sums, and slower.
+ * Shape rules: as sq_kv_paged_append; table_width * page_size < 2^30. */
+size_t sq_kv_attention_workspace_bytes(int64_t T, int hq, int max_q, const sq_kv_pages* pages);
+sq_status sq_kv_paged_attention(const void* q, int64_t q_stride, int64_t T, int hq,
+                                const sq_kv_pages* pages, const int32_t* block_table,
+                                int table_width, const int32_t* cu_seqlens,
+                                const int32_t* lengths, int B, int max_q,
+                                const sq_score_rule* rule, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* sq_kv_prefix_attention -- sq_kv_paged_attention for sequences that share a
+ * prefix: positions 0 .. prefix_len - 1 are the rows of the pages
+ * prefix_table (device int32 [ceil(prefix_len / page_size)]), the same for
+ * all, and sequence b's own cache row j (lengths[b] of them, in its
+ * block_table) is position prefix_len + j.  The shared rows are read once for
+ * the batch.  prefix_len (host) is 1 .. 2^30 - 1; lengths[b] may be 0.  All
+ * else as sq_kv_paged_attention; keys appended behind a prefix need their
+ * rotary positions shifted by prefix_len (a table that starts there). */
+sq_status sq_kv_prefix_attention(const void* q, int64_t q_stride, int64_t T, int hq,
+                                 const sq_kv_pages* pages, const int32_t* prefix_table,
+                                 int64_t prefix_len, const int32_t* block_table, int table_width,
+                                 const int32_t* cu_seqlens, const int32_t* lengths, int B,
+                                 int max_q, const sq_score_rule* rule, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -494,6 +494,78 @@ def kv8_decode_attention(q, k_cache, k_scale, k_zero, v_cache, v_scale, v_zero,
 
 
 # ---------------------------------------------------------------------------
+# The paged cache: the head maps of its append (per-head RMS norm, rotary
+# embedding of a part of the head in either layout, R3), and causal attention
+# of a sequence's new tokens with capped, biased or windowed scores.  Serving
+# forms of the path above; the pages have no counterpart beyond Q5's sites.
+# ---------------------------------------------------------------------------
+
+
+def rms_norm(x: np.ndarray, w, eps: float) -> np.ndarray:
+    """x * w / sqrt(mean(x^2) + eps) over the last axis; x itself without a weight."""
+    x = np.asarray(x, np.float64)
+    if w is None:
+        return x
+    return x * np.asarray(w, np.float64) / np.sqrt(np.mean(x * x, axis=-1, keepdims=True) + eps)
+
+
+def rope_part(x: np.ndarray, pos: np.ndarray, cos, sin, interleaved: bool) -> np.ndarray:
+    """Rotary embedding of the first 2 * cos.shape[1] channels of x [T, h, d]."""
+    x = np.asarray(x, np.float64)
+    if cos is None:
+        return x
+    n = cos.shape[1]
+    c = np.asarray(cos, np.float64)[pos][:, None, :]
+    s = np.asarray(sin, np.float64)[pos][:, None, :]
+    first, second = (slice(0, 2 * n, 2), slice(1, 2 * n, 2)) if interleaved \
+        else (slice(0, n), slice(n, 2 * n))
+    y = x.copy()
+    y[..., first] = x[..., first] * c - x[..., second] * s
+    y[..., second] = x[..., second] * c + x[..., first] * s
+    return y
+
+
+def head_forward(x, w, eps, pos, cos, sin, interleaved) -> np.ndarray:
+    """Norm, rotary embedding, head-wise Hadamard (float64)."""
+    return headwise_hadamard(rope_part(rms_norm(x, w, eps), pos, cos, sin, interleaved))
+
+
+def causal_attention(q, K, V, qpos, kpos, scale=None, softcap=0.0, window=0, slopes=None):
+    """q [n, hq, d] at positions qpos over K, V [S, hkv, d] at kpos -> (out [n, hq, d],
+    lse [n, hq], spread [n, hq, d] = sum_j p_j |v_j|, size = largest sum_d |q_d k_d| * scale)."""
+    q, K, V = (np.asarray(a, np.float64) for a in (q, K, V))
+    n, hq, d = q.shape
+    group = hq // K.shape[1]
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    out, spread = np.zeros((n, hq, d)), np.zeros((n, hq, d))
+    lse = np.full((n, hq), -np.inf)
+    dist = np.asarray(qpos)[:, None] - np.asarray(kpos)[None]
+    seen = dist >= 0
+    if window:
+        seen &= dist < window
+    live = seen.any(axis=1)
+    size = 0.0
+    for h in range(hq):
+        s = scale * (q[:, h] @ K[:, h // group].T)
+        if s.size:
+            size = max(size, float((abs(scale) * (np.abs(q[:, h]) @ np.abs(K[:, h // group]).T)).max()))
+        if softcap:
+            s = softcap * np.tanh(s / softcap)
+        if slopes is not None:
+            s = s - float(slopes[h]) * dist
+        s = np.where(seen, s, -np.inf)[live]
+        if not s.size:
+            continue
+        m = s.max(axis=1, keepdims=True)
+        p = np.exp(s - m)
+        total = p.sum(axis=1, keepdims=True)
+        lse[live, h] = (m + np.log(total))[:, 0]
+        out[live, h] = (p / total) @ V[:, h // group]
+        spread[live, h] = (p / total) @ np.abs(V[:, h // group])
+    return out, lse, spread, size
+
+
+# ---------------------------------------------------------------------------
 # Cayley SGD for the head-wise rotation R2 ("SpinQuant, Reproduced", Q6).
 # The pages give the transform R' = (I - a/2 Y)^-1 (I + a/2 Y) R with a skew
 # Y, a straight-through estimator through the quantizers, and the objective:

@@ -11,6 +11,8 @@ Entry points (same names as the C ABI without the ``sq_`` prefix):
   w4a4_workspace_bytes, kv_rotate_quant,
   kv_dequant, kv4_decode_attention, kv4_decode_workspace_bytes, rope_tables,
   kv_rotate_quant8, kv8_dequant, kv8_decode_attention,
+  KVPages, kv_paged_append, kv_paged_dequant, kv_paged_attention, kv_prefix_attention,
+  kv_attention_workspace_bytes,
   R2Problem (sq_r2_prepare / sq_r2_loss_grad / sq_r2_cayley_learn), cayley_update,
   r2_random_hadamard, orth_error,
   device_status, debug_set_spin_limit.
@@ -18,6 +20,7 @@ Entry points (same names as the C ABI without the ``sq_`` prefix):
 from __future__ import annotations
 
 from .binding import (  # noqa: F401
+    KVPages,
     R2Problem,
     cayley_update,
     orth_error,
@@ -35,7 +38,12 @@ from .binding import (  # noqa: F401
     kv4_decode_workspace_bytes,
     kv8_decode_attention,
     kv8_dequant,
+    kv_attention_workspace_bytes,
     kv_dequant,
+    kv_paged_append,
+    kv_paged_attention,
+    kv_paged_dequant,
+    kv_prefix_attention,
     kv_rotate_quant,
     kv_rotate_quant8,
     lib,

@@ -6,6 +6,7 @@ goes straight to the matching ``sq_*`` entry point on torch's current stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -86,6 +87,34 @@ lib.sq_orth_error.restype = _i32
 lib.sq_orth_error.argtypes = [_vp, _i32, _i32, _vp, _vp]
 lib.sq_rope_tables.restype = _i32
 lib.sq_rope_tables.argtypes = [ctypes.c_double, _i32, _i32, _vp, _vp, _vp]
+
+
+class _PagesStruct(ctypes.Structure):
+    """``sq_kv_pages``."""
+    _fields_ = [("k_codes", _vp), ("k_scale", _vp), ("k_zero", _vp), ("v_codes", _vp),
+                ("v_scale", _vp), ("v_zero", _vp), ("num_pages", _i64), ("page_size", _i32),
+                ("hkv", _i32), ("d", _i32), ("bits", _i32)]
+
+
+class _ScoreRule(ctypes.Structure):
+    """``sq_score_rule``."""
+    _fields_ = [("scale", _f32), ("softcap", _f32), ("window", _i32), ("slopes", _vp)]
+
+
+lib.sq_kv_paged_append.restype = _i32
+lib.sq_kv_paged_append.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _i32,
+                                   _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _f32,
+                                   _vp, _vp]
+lib.sq_kv_paged_dequant.restype = _i32
+lib.sq_kv_paged_dequant.argtypes = [_vp, _vp, _i32, _vp, _vp, _i32, _i64, _vp, _vp, _vp]
+lib.sq_kv_attention_workspace_bytes.restype = ctypes.c_size_t
+lib.sq_kv_attention_workspace_bytes.argtypes = [_i64, _i32, _i32, _vp]
+lib.sq_kv_paged_attention.restype = _i32
+lib.sq_kv_paged_attention.argtypes = [_vp, _i64, _i64, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _i32,
+                                      _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+lib.sq_kv_prefix_attention.restype = _i32
+lib.sq_kv_prefix_attention.argtypes = [_vp, _i64, _i64, _i32, _vp, _vp, _i64, _vp, _i32, _vp, _vp,
+                                       _i32, _i32, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
 lib.sq_device_status.restype = _i32
 lib.sq_device_status.argtypes = [_vp]
 lib.sq_debug_set_spin_limit.restype = None
@@ -291,7 +320,7 @@ def _reset_workspaces(device_index: int) -> None:
     ran out (SQ_ERR_TIMEOUT) can leave partial sums and arrival counters in
     it, which the next call would otherwise add to."""
     with _ws_lock:
-        bufs = [b for (d, _), b in _ws_cache.items() if d == device_index]
+        bufs = [b for (d, *_), b in _ws_cache.items() if d == device_index]
     if bufs:
         torch.cuda.synchronize(device_index)
         for b in bufs:
@@ -577,6 +606,285 @@ def kv8_dequant(cache: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor, ou
     st = lib.sq_kv8_dequant(cache.data_ptr(), scale.data_ptr(), zero.data_ptr(), T, h, d,
                             out.data_ptr(), _stream(cache))
     _check(st, "sq_kv8_dequant")
+    return out
+
+
+class KVPages:
+    """A pool of pages of the 4- or 8-bit KV cache (``sq_kv_pages``).
+
+    k_codes, v_codes: CUDA uint8 [num_pages, hkv, page_size, 64] (4 bits, two
+    codes per byte) or [..., 128] (8 bits); k_scale, v_scale float32 and
+    k_zero, v_zero uint8 [num_pages, hkv, page_size].  ``KVPages.empty``
+    allocates them.  The object keeps the tensors alive and nothing else; which
+    page belongs to which sequence is the caller's block table.
+    """
+
+    def __init__(self, k_codes: torch.Tensor, k_scale: torch.Tensor, k_zero: torch.Tensor,
+                 v_codes: torch.Tensor, v_scale: torch.Tensor, v_zero: torch.Tensor):
+        if not isinstance(k_codes, torch.Tensor) or k_codes.dim() != 4:
+            raise ValueError("k_codes must be a tensor [num_pages, hkv, page_size, bytes]")
+        n, hkv, ps, rb = k_codes.shape
+        if rb not in (64, 128):
+            raise ValueError("a row of codes must hold 64 bytes (4 bits) or 128 (8 bits), got %d" % rb)
+        if n < 1 or not 1 <= hkv <= 64 or not 16 <= ps <= 4096 or ps & (ps - 1):
+            raise ValueError("need at least one page, 1..64 KV heads and a page size that is a "
+                             "power of two from 16 to 4096, got %s" % (tuple(k_codes.shape),))
+        for nm, c, sc, z in (("k", k_codes, k_scale, k_zero), ("v", v_codes, v_scale, v_zero)):
+            _expect(c, nm + "_codes", torch.uint8, (n, hkv, ps, rb))
+            _expect(sc, nm + "_scale", torch.float32, (n, hkv, ps))
+            _expect(z, nm + "_zero", torch.uint8, (n, hkv, ps))
+        self._tensors = (k_codes, k_scale, k_zero, v_codes, v_scale, v_zero)
+        _same_device(*self._tensors)
+        self.k_codes, self.k_scale, self.k_zero = k_codes, k_scale, k_zero
+        self.v_codes, self.v_scale, self.v_zero = v_codes, v_scale, v_zero
+        self.num_pages, self.hkv, self.page_size = n, hkv, ps
+        self.bits = rb // 16
+        self.device = k_codes.device
+        self._struct = _PagesStruct(*(t.data_ptr() for t in self._tensors), n, ps, hkv, 128,
+                                    self.bits)
+        self._ref = ctypes.addressof(self._struct)
+        self._ws_bytes = {}
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, hkv: int, bits: int = 4, device=None):
+        """A pool of `num_pages` pages, zero-filled."""
+        if bits not in (4, 8):
+            raise ValueError("bits must be 4 or 8")
+        device = torch.device("cuda") if device is None else torch.device(device)
+        shape = (num_pages, hkv, page_size)
+        parts = []
+        for _ in range(2):
+            parts += [torch.zeros(shape + (16 * bits,), dtype=torch.uint8, device=device),
+                      torch.zeros(shape, dtype=torch.float32, device=device),
+                      torch.zeros(shape, dtype=torch.uint8, device=device)]
+        return cls(*parts)
+
+
+def _heads(t, name, heads=None):
+    """A bf16 tensor [T, heads, 128] whose heads are contiguous; returns its token stride."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError("%s must be a bf16 tensor [T, heads, 128]" % name)
+    T, h, d = t.shape
+    if d != 128 or (heads is not None and h != heads):
+        raise ValueError("%s must have shape [T, %s, 128], got %s"
+                         % (name, "heads" if heads is None else heads, tuple(t.shape)))
+    s = t.stride()
+    if s[2] != 1 or (s[1] != 128 and h > 1):
+        raise ValueError("%s must have contiguous heads (only the token stride is free)" % name)
+    if T <= 1:
+        return h * 128
+    if s[0] < h * 128 or s[0] % 8:
+        raise ValueError("%s needs a token stride that is a multiple of 8 and holds its heads, got %d"
+                         % (name, s[0]))
+    return s[0]
+
+
+def _expect_batch(pages, block_table, cu_seqlens, lengths, lname):
+    if not isinstance(pages, KVPages):
+        raise TypeError("pages must be a KVPages")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.shape[1] < 1:
+        raise ValueError("block_table must be int32 [B, pages per sequence]")
+    B, width = block_table.shape
+    _expect(block_table, "block_table", torch.int32, (B, width))
+    _expect(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
+    _expect(lengths, lname, torch.int32, (B,))
+    return B, width
+
+
+def _on_device(device):
+    """Makes `device` current around a C call (the library launches on the current device)."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def kv_paged_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pages: KVPages,
+                    block_table: torch.Tensor, cu_seqlens: torch.Tensor, cached: torch.Tensor,
+                    cos: torch.Tensor = None, sin: torch.Tensor = None, interleaved: bool = False,
+                    q_norm: torch.Tensor = None, k_norm: torch.Tensor = None, eps: float = 1e-6,
+                    q_out: torch.Tensor = None):
+    """New tokens of a ragged batch into the paged cache (``sq_kv_paged_append``).
+
+    Per-head RMS norm of q and k (with q_norm, k_norm float32 [128]), rotary
+    embedding of the first channels (cos, sin float32 [max_pos, rot / 2]; half
+    or interleaved pairs), R3, quantization of k and v into the pages.
+
+    q bf16 [T, hq, 128], k and v bf16 [T, hkv, 128] (any token stride that is a
+    multiple of 8); block_table int32 [B, pages]; cu_seqlens int32 [B + 1];
+    cached int32 [B], the tokens already cached.  Returns the rotated queries,
+    bf16 [T, hq, 128]; rows behind cu_seqlens[B] are not written.
+    """
+    B, width = _expect_batch(pages, block_table, cu_seqlens, cached, "cached")
+    sq_ = _heads(q, "q")
+    T, hq = q.shape[0], q.shape[1]
+    sk, sv = _heads(k, "k", pages.hkv), _heads(v, "v", pages.hkv)
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError("q, k and v must hold the same number of tokens")
+    if hq % pages.hkv or hq > 256:
+        raise ValueError("query heads must be a multiple of the %d KV heads, at most 256" % pages.hkv)
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin must both be given or both be None")
+    rot = max_pos = 0
+    if cos is not None:
+        if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
+            raise ValueError("cos must be [max_pos, rot / 2]")
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        if rot % 16 or not 16 <= rot <= 128:
+            raise ValueError("rotated channels must be a multiple of 16 from 16 to 128, got %d" % rot)
+        _expect(cos, "cos", torch.float32, (max_pos, rot // 2))
+        _expect(sin, "sin", torch.float32, (max_pos, rot // 2))
+    for t, nm in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if t is not None:
+            _expect(t, nm, torch.float32, (128,))
+    if q_out is not None:
+        _expect(q_out, "q_out", torch.bfloat16, (T, hq, 128))
+    _same_device(q, k, v, block_table, cu_seqlens, cached, cos, sin, q_norm, k_norm, q_out,
+                 pages.k_codes)
+    _need_cuda(q, pages.k_codes)
+    if q_out is None:
+        q_out = torch.empty((T, hq, 128), dtype=torch.bfloat16, device=q.device)
+    with _on_device(q.device):
+        st = lib.sq_kv_paged_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), sq_, sk, sv, T, hq,
+                                    pages._ref, block_table.data_ptr(), width,
+                                    cu_seqlens.data_ptr(), cached.data_ptr(), B, _ptr(cos),
+                                    _ptr(sin), max_pos, rot, int(bool(interleaved)), _ptr(q_norm),
+                                    _ptr(k_norm), float(eps), q_out.data_ptr(), _stream(q))
+    _check(st, "sq_kv_paged_append")
+    return q_out
+
+
+def kv_paged_dequant(pages: KVPages, block_table: torch.Tensor, cu_seqlens: torch.Tensor,
+                     cached: torch.Tensor, num_tokens: int, k_out: torch.Tensor = None,
+                     v_out: torch.Tensor = None):
+    """Rows of the paged cache back to bf16 (``sq_kv_paged_dequant``): for the
+    tokens that kv_paged_append wrote with the same arguments, or with cached
+    = 0 for whole sequences.  Returns (k, v) bf16 [num_tokens, hkv, 128]; rows
+    behind cu_seqlens[B] are not written.
+    """
+    B, width = _expect_batch(pages, block_table, cu_seqlens, cached, "cached")
+    shape = (int(num_tokens), pages.hkv, 128)
+    for t, nm in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None:
+            _expect(t, nm, torch.bfloat16, shape)
+    _same_device(block_table, cu_seqlens, cached, k_out, v_out, pages.k_codes)
+    _need_cuda(block_table, pages.k_codes)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=pages.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=pages.device)
+    with _on_device(pages.device):
+        st = lib.sq_kv_paged_dequant(pages._ref, block_table.data_ptr(), width,
+                                     cu_seqlens.data_ptr(), cached.data_ptr(), B, shape[0],
+                                     k_out.data_ptr(), v_out.data_ptr(), _stream(block_table))
+    _check(st, "sq_kv_paged_dequant")
+    return k_out, v_out
+
+
+def kv_attention_workspace_bytes(T: int, hq: int, max_q: int, pages: KVPages) -> int:
+    """Scratch bytes that let the paged attention calls split keys across CTAs."""
+    return int(lib.sq_kv_attention_workspace_bytes(int(T), int(hq), int(max_q), pages._ref))
+
+
+def kv_paged_attention(q: torch.Tensor, pages: KVPages, block_table: torch.Tensor,
+                       cu_seqlens: torch.Tensor, lengths: torch.Tensor, max_q: int,
+                       scale: float = None, softcap: float = 0.0, window: int = 0,
+                       slopes: torch.Tensor = None, out: torch.Tensor = None,
+                       lse: torch.Tensor = None, workspace: torch.Tensor = None):
+    """Causal attention of a ragged batch's new tokens over the paged cache
+    (``sq_kv_paged_attention``).
+
+    q bf16 [T, hq, 128] (what kv_paged_append returned); lengths int32 [B], the
+    cached tokens with the new ones; max_q, the most new tokens of a sequence.
+    scale defaults to 1/sqrt(128); softcap caps scores by a tanh; window hides
+    keys that far back; slopes (float32 [hq]) subtract slope x distance.
+    Returns bf16 [T, hq, 128]; lse (float32 [T, hq]), where given, is written.
+    Without ``workspace`` a cached buffer of the stream is used; under stream
+    capture, one that belongs to the graph.
+    """
+    return _kv_attention(q, pages, None, 0, block_table, cu_seqlens, lengths, max_q, scale,
+                         softcap, window, slopes, out, lse, workspace)
+
+
+def kv_prefix_attention(q: torch.Tensor, pages: KVPages, prefix_table: torch.Tensor,
+                        prefix_len: int, block_table: torch.Tensor, cu_seqlens: torch.Tensor,
+                        lengths: torch.Tensor, max_q: int, scale: float = None,
+                        softcap: float = 0.0, window: int = 0, slopes: torch.Tensor = None,
+                        out: torch.Tensor = None, lse: torch.Tensor = None,
+                        workspace: torch.Tensor = None):
+    """kv_paged_attention behind a shared prefix (``sq_kv_prefix_attention``):
+    the first prefix_len positions of every sequence are the rows of the pages
+    prefix_table (int32 [pages]); lengths counts each sequence's own rows
+    behind them.  The prefix is read once for the batch.
+    """
+    if not isinstance(prefix_table, torch.Tensor) or prefix_table.dim() != 1:
+        raise ValueError("prefix_table must be int32 [pages]")
+    _expect(prefix_table, "prefix_table", torch.int32, tuple(prefix_table.shape))
+    if not isinstance(pages, KVPages):
+        raise TypeError("pages must be a KVPages")
+    prefix_len = int(prefix_len)
+    if not 1 <= prefix_len <= prefix_table.shape[0] * pages.page_size:
+        raise ValueError("prefix_len must be 1 .. %d (the rows of prefix_table's pages), got %d"
+                         % (prefix_table.shape[0] * pages.page_size, prefix_len))
+    return _kv_attention(q, pages, prefix_table, prefix_len, block_table, cu_seqlens, lengths,
+                         max_q, scale, softcap, window, slopes, out, lse, workspace)
+
+
+def _attention_workspace(device, stream, need):
+    # a graph gets a workspace of its own, zeroed by the graph: a cached one
+    # would be shared by graphs that may replay at the same time
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros((need,), dtype=torch.uint8, device=device)
+    key = (device.index, stream, "attention")
+    with _ws_lock:
+        buf = _ws_cache.get(key)
+        if buf is None or buf.numel() < need:
+            buf = torch.zeros((need,), dtype=torch.uint8, device=device)
+            _ws_cache[key] = buf
+        return buf
+
+
+def _kv_attention(q, pages, prefix_table, prefix_len, block_table, cu_seqlens, lengths, max_q,
+                  scale, softcap, window, slopes, out, lse, workspace):
+    B, width = _expect_batch(pages, block_table, cu_seqlens, lengths, "lengths")
+    stride = _heads(q, "q")
+    T, hq = q.shape[0], q.shape[1]
+    if hq % pages.hkv or hq > 256:
+        raise ValueError("query heads must be a multiple of the %d KV heads, at most 256" % pages.hkv)
+    if slopes is not None:
+        _expect(slopes, "slopes", torch.float32, (hq,))
+    if out is not None:
+        _expect(out, "out", torch.bfloat16, (T, hq, 128))
+    if lse is not None:
+        _expect(lse, "lse", torch.float32, (T, hq))
+    _expect_workspace(workspace)
+    _same_device(q, block_table, cu_seqlens, lengths, prefix_table, slopes, out, lse, workspace,
+                 pages.k_codes)
+    _need_cuda(q, pages.k_codes)
+    if out is None:
+        out = torch.empty((T, hq, 128), dtype=torch.bfloat16, device=q.device)
+    rule = _ScoreRule(128 ** -0.5 if scale is None else float(scale), float(softcap), int(window),
+                      _ptr(slopes))
+    max_q = int(max_q)
+    with _on_device(q.device):
+        stream = _stream(q)
+        if workspace is None:
+            key = (T, hq, max_q)
+            need = pages._ws_bytes.get(key)
+            if need is None:
+                need = pages._ws_bytes[key] = kv_attention_workspace_bytes(T, hq, max_q, pages)
+            workspace = _attention_workspace(q.device, stream, need) if need else None
+        ws_ptr = None if workspace is None else workspace.data_ptr()
+        ws_bytes = 0 if workspace is None else workspace.numel()
+        args = (block_table.data_ptr(), width, cu_seqlens.data_ptr(), lengths.data_ptr(), B, max_q,
+                ctypes.addressof(rule), out.data_ptr(), _ptr(lse), ws_ptr, ws_bytes, stream)
+        if prefix_table is None:
+            st = lib.sq_kv_paged_attention(q.data_ptr(), stride, T, hq, pages._ref, *args)
+            name = "sq_kv_paged_attention"
+        else:
+            st = lib.sq_kv_prefix_attention(q.data_ptr(), stride, T, hq, pages._ref,
+                                            prefix_table.data_ptr(), prefix_len, *args)
+            name = "sq_kv_prefix_attention"
+    _check(st, name)
     return out
 
 

@@ -93,6 +93,7 @@ using sq::host::set_error;
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
 sq_status precheck_device() {
@@ -308,6 +309,202 @@ sq_status sq_kv8_decode_attention(const void* q, const uint8_t* k_cache, const f
                              S_max, hq, hkv, d, out, workspace, workspace_bytes, 8, stream);
 }
 
+// ---------------------------------------------------------------- paged KV
+
+static sq_status check_pages(const sq_kv_pages* p, int hq) {
+  if (!p) {
+    set_error("pages is null");
+    return SQ_ERR_INVALID_ARG;
+  }
+  if (p->d != 128 || (p->bits != 4 && p->bits != 8) || p->hkv < 1 || p->hkv > 64 ||
+      p->page_size < 16 || p->page_size > 4096 || (p->page_size & (p->page_size - 1)) ||
+      p->num_pages < 1 || p->num_pages > 0x7fffffffLL) {
+    set_error("unsupported pages: d=%d bits=%d hkv=%d page_size=%d num_pages=%lld (need d == 128, "
+              "4 or 8 bits, hkv 1..64, a page size that is a power of two from 16 to 4096)",
+              p->d, p->bits, p->hkv, p->page_size, (long long)p->num_pages);
+    return SQ_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (hq < 1 || hq > 256 || hq % p->hkv) {
+    set_error("unsupported heads hq=%d hkv=%d (need 1 <= hq <= 256, a multiple of hkv)", hq,
+              p->hkv);
+    return SQ_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (!p->k_codes || !p->k_scale || !p->k_zero || !p->v_codes || !p->v_scale || !p->v_zero) {
+    set_error("null pointer in pages");
+    return SQ_ERR_INVALID_ARG;
+  }
+  if (!aligned16(p->k_codes) || !aligned16(p->k_scale) || !aligned16(p->k_zero) ||
+      !aligned16(p->v_codes) || !aligned16(p->v_scale) || !aligned16(p->v_zero)) {
+    set_error("the page arrays must be 16-byte aligned");
+    return SQ_ERR_MISALIGNED;
+  }
+  return SQ_OK;
+}
+
+static sq_status check_batch(const sq_kv_pages* p, int64_t T, int B, int width) {
+  if (T < 0 || B < 0 || width < 1) {
+    set_error("bad sizes T=%lld B=%d table_width=%d", (long long)T, B, width);
+    return SQ_ERR_INVALID_ARG;
+  }
+  if (T > 0x7fffffffLL || B > (1 << 20) ||
+      static_cast<int64_t>(width) * p->page_size >= (1LL << 30)) {
+    set_error("unsupported sizes T=%lld B=%d table_width=%d page_size=%d (need T < 2^31, "
+              "B <= 2^20, table_width * page_size < 2^30)",
+              (long long)T, B, width, p->page_size);
+    return SQ_ERR_UNSUPPORTED_SHAPE;
+  }
+  return SQ_OK;
+}
+
+static bool stride_ok(int64_t stride, int heads) {
+  return stride >= static_cast<int64_t>(heads) * 128 && stride % 8 == 0 && stride < (1LL << 31);
+}
+
+sq_status sq_kv_paged_append(const void* q, const void* k, const void* v, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, int64_t T, int hq,
+                             const sq_kv_pages* pages, const int32_t* block_table,
+                             int table_width, const int32_t* cu_seqlens, const int32_t* cached,
+                             int B, const float* rope_cos, const float* rope_sin, int max_pos,
+                             int rot, int interleaved, const float* q_norm, const float* k_norm,
+                             float eps, void* q_out, void* stream) {
+  sq_status st = check_pages(pages, hq);
+  if (st == SQ_OK) st = check_batch(pages, T, B, table_width);
+  if (st != SQ_OK) return st;
+  if ((rope_cos == nullptr) != (rope_sin == nullptr) || (rope_cos && max_pos < 1) ||
+      !(eps >= 0.f) || eps > 3.0e38f || (interleaved != 0 && interleaved != 1)) {
+    set_error("need both rope tables or none, max_pos >= 1 with them, a finite eps >= 0 and "
+              "interleaved 0 or 1 (max_pos=%d eps=%g interleaved=%d)",
+              max_pos, (double)eps, interleaved);
+    return SQ_ERR_INVALID_ARG;
+  }
+  if (rope_cos && (rot < 16 || rot > 128 || rot % 16)) {
+    set_error("unsupported rot=%d (need a multiple of 16 from 16 to 128)", rot);
+    return SQ_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (!stride_ok(q_stride, hq) || !stride_ok(k_stride, pages->hkv) ||
+      !stride_ok(v_stride, pages->hkv)) {
+    set_error("unsupported token strides %lld, %lld, %lld (need multiples of 8 that hold the heads)",
+              (long long)q_stride, (long long)k_stride, (long long)v_stride);
+    return SQ_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (T == 0 || B == 0) return SQ_OK;
+  if (!q || !k || !v || !block_table || !cu_seqlens || !cached || !q_out) {
+    set_error("null pointer argument");
+    return SQ_ERR_INVALID_ARG;
+  }
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
+      !aligned4(block_table) || !aligned4(cu_seqlens) || !aligned4(cached) ||
+      !aligned16(rope_cos) || !aligned16(rope_sin) || !aligned16(q_norm) || !aligned16(k_norm)) {
+    set_error("device pointers must be 16-byte aligned (int32 arrays, slopes and lse: 4-byte)");
+    return SQ_ERR_MISALIGNED;
+  }
+  st = precheck_device();
+  if (st != SQ_OK) return st;
+  return sq::paged::run_append(q, k, v, q_stride, k_stride, v_stride, T, hq, *pages, block_table,
+                               table_width, cu_seqlens, cached, B, rope_cos, rope_sin, max_pos, rot,
+                               interleaved, q_norm, k_norm, eps, q_out,
+                               static_cast<cudaStream_t>(stream));
+}
+
+sq_status sq_kv_paged_dequant(const sq_kv_pages* pages, const int32_t* block_table,
+                              int table_width, const int32_t* cu_seqlens, const int32_t* cached,
+                              int B, int64_t T, void* k_out, void* v_out, void* stream) {
+  sq_status st = check_pages(pages, pages ? pages->hkv : 1);
+  if (st == SQ_OK) st = check_batch(pages, T, B, table_width);
+  if (st != SQ_OK) return st;
+  if (T == 0 || B == 0) return SQ_OK;
+  if (!block_table || !cu_seqlens || !cached || !k_out || !v_out) {
+    set_error("null pointer argument");
+    return SQ_ERR_INVALID_ARG;
+  }
+  if (!aligned4(block_table) || !aligned4(cu_seqlens) || !aligned4(cached) ||
+      !aligned16(k_out) || !aligned16(v_out)) {
+    set_error("device pointers must be 16-byte aligned (int32 arrays, slopes and lse: 4-byte)");
+    return SQ_ERR_MISALIGNED;
+  }
+  st = precheck_device();
+  if (st != SQ_OK) return st;
+  return sq::paged::run_dequant(*pages, block_table, table_width, cu_seqlens, cached, B, T, k_out,
+                                v_out, static_cast<cudaStream_t>(stream));
+}
+
+size_t sq_kv_attention_workspace_bytes(int64_t T, int hq, int max_q, const sq_kv_pages* pages) {
+  if (check_pages(pages, hq) != SQ_OK || T <= 0 || max_q <= 0) return 0;
+  if (sq::host::current_device() < 0) return 0;
+  return sq::paged::attention_workspace_bytes(T, hq, pages->hkv, max_q, pages->bits);
+}
+
+static sq_status paged_attention(const void* q, int64_t q_stride, int64_t T, int hq,
+                                 const sq_kv_pages* pages, const int32_t* prefix_table,
+                                 int64_t prefix_len, const int32_t* block_table, int table_width,
+                                 const int32_t* cu_seqlens, const int32_t* lengths, int B,
+                                 int max_q, const sq_score_rule* rule, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  sq_status st = check_pages(pages, hq);
+  if (st == SQ_OK) st = check_batch(pages, T, B, table_width);
+  if (st != SQ_OK) return st;
+  if (!rule || max_q < 0) {
+    set_error("rule is null or max_q=%d is negative", max_q);
+    return SQ_ERR_INVALID_ARG;
+  }
+  if (!(rule->scale > -3.0e38f && rule->scale < 3.0e38f) ||
+      !(rule->softcap >= 0.f && rule->softcap < 3.0e38f) || rule->window < 0 ||
+      rule->window > (1 << 30)) {
+    set_error("bad score rule: scale=%g softcap=%g window=%d", (double)rule->scale,
+              (double)rule->softcap, rule->window);
+    return SQ_ERR_INVALID_ARG;
+  }
+  if (!stride_ok(q_stride, hq)) {
+    set_error("unsupported token stride %lld (need a multiple of 8 that holds the heads)",
+              (long long)q_stride);
+    return SQ_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (T == 0 || B == 0 || max_q == 0) return SQ_OK;
+  if (!q || !block_table || !cu_seqlens || !lengths || !out || (prefix_len > 0 && !prefix_table)) {
+    set_error("null pointer argument");
+    return SQ_ERR_INVALID_ARG;
+  }
+  if (!aligned16(q) || !aligned16(out) || !aligned4(lse) || !aligned4(block_table) ||
+      !aligned4(cu_seqlens) || !aligned4(lengths) || !aligned4(prefix_table) ||
+      !aligned4(rule->slopes) || !aligned16(workspace)) {
+    set_error("device pointers must be 16-byte aligned (int32 arrays, slopes and lse: 4-byte)");
+    return SQ_ERR_MISALIGNED;
+  }
+  st = precheck_device();
+  if (st != SQ_OK) return st;
+  return sq::paged::run_attention(q, q_stride, T, hq, *pages, prefix_table,
+                                  static_cast<int>(prefix_len), block_table, table_width,
+                                  cu_seqlens, lengths, B, max_q, *rule, out, lse, workspace,
+                                  workspace ? workspace_bytes : 0,
+                                  static_cast<cudaStream_t>(stream));
+}
+
+sq_status sq_kv_paged_attention(const void* q, int64_t q_stride, int64_t T, int hq,
+                                const sq_kv_pages* pages, const int32_t* block_table,
+                                int table_width, const int32_t* cu_seqlens,
+                                const int32_t* lengths, int B, int max_q,
+                                const sq_score_rule* rule, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  return paged_attention(q, q_stride, T, hq, pages, nullptr, 0, block_table, table_width,
+                         cu_seqlens, lengths, B, max_q, rule, out, lse, workspace, workspace_bytes,
+                         stream);
+}
+
+sq_status sq_kv_prefix_attention(const void* q, int64_t q_stride, int64_t T, int hq,
+                                 const sq_kv_pages* pages, const int32_t* prefix_table,
+                                 int64_t prefix_len, const int32_t* block_table, int table_width,
+                                 const int32_t* cu_seqlens, const int32_t* lengths, int B,
+                                 int max_q, const sq_score_rule* rule, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (prefix_len < 1 || prefix_len >= (1LL << 30)) {
+    set_error("prefix_len=%lld is not in 1 .. 2^30 - 1", (long long)prefix_len);
+    return SQ_ERR_INVALID_ARG;
+  }
+  return paged_attention(q, q_stride, T, hq, pages, prefix_table, prefix_len, block_table,
+                         table_width, cu_seqlens, lengths, B, max_q, rule, out, lse, workspace,
+                         workspace_bytes, stream);
+}
+
 size_t sq_w4a4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N < 16 || N % 16 || K < 128 || K % 128 || K > 65536) return 0;
   if (sq::host::current_device() < 0) return 0;
@@ -345,7 +542,7 @@ sq_status sq_w4a4_linear(const uint8_t* a_q, const float* a_scale, const uint8_t
   }
   if (!aligned16(a_q) || !aligned16(a_scale) || !aligned16(w_q) || !aligned16(w_scale) ||
       !aligned16(out) || (workspace && !aligned16(workspace))) {
-    set_error("device pointers must be 16-byte aligned");
+    set_error("device pointers must be 16-byte aligned (int32 arrays, slopes and lse: 4-byte)");
     return SQ_ERR_MISALIGNED;
   }
   sq_status st = precheck_device();
@@ -380,7 +577,7 @@ sq_status sq_w4a8_linear(const int8_t* a_q, const float* a_scale, const uint8_t*
   }
   if (!aligned16(a_q) || !aligned16(a_scale) || !aligned16(w_q) || !aligned16(w_scale) ||
       !aligned16(out) || (workspace && !aligned16(workspace))) {
-    set_error("device pointers must be 16-byte aligned");
+    set_error("device pointers must be 16-byte aligned (int32 arrays, slopes and lse: 4-byte)");
     return SQ_ERR_MISALIGNED;
   }
   sq_status st = precheck_device();
@@ -425,7 +622,7 @@ static sq_status kv_rotate_quant(const void* q, const void* k, const void* v, in
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
       !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale) ||
       !aligned16(pos) || (rope_cos && (!aligned16(rope_cos) || !aligned16(rope_sin)))) {
-    set_error("device pointers must be 16-byte aligned");
+    set_error("device pointers must be 16-byte aligned (int32 arrays, slopes and lse: 4-byte)");
     return SQ_ERR_MISALIGNED;
   }
   sq_status st = precheck_device();
@@ -471,7 +668,7 @@ static sq_status kv_dequant(const uint8_t* cache, const float* scale, const uint
     return SQ_ERR_INVALID_ARG;
   }
   if (!aligned16(cache) || !aligned16(scale) || !aligned16(out_bf16)) {
-    set_error("device pointers must be 16-byte aligned");
+    set_error("device pointers must be 16-byte aligned (int32 arrays, slopes and lse: 4-byte)");
     return SQ_ERR_MISALIGNED;
   }
   sq_status st = precheck_device();
@@ -614,7 +811,7 @@ sq_status sq_cayley_update(const double* R, const double* G, double alpha, int n
   }
   if (!aligned16(R) || !aligned16(G) || !aligned16(R_out) || !aligned16(workspace) ||
       (R_out_f32 && !aligned16(R_out_f32))) {
-    set_error("device pointers must be 16-byte aligned");
+    set_error("device pointers must be 16-byte aligned (int32 arrays, slopes and lse: 4-byte)");
     return SQ_ERR_MISALIGNED;
   }
   sq_status st = precheck_device();
@@ -672,7 +869,7 @@ sq_status sq_rope_tables(double theta, int max_pos, int d, float* cos, float* si
     return SQ_ERR_INVALID_ARG;
   }
   if (!aligned16(cos) || !aligned16(sin)) {
-    set_error("device pointers must be 16-byte aligned");
+    set_error("device pointers must be 16-byte aligned (int32 arrays, slopes and lse: 4-byte)");
     return SQ_ERR_MISALIGNED;
   }
   sq_status st = precheck_device();

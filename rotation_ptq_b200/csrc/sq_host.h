@@ -138,4 +138,25 @@ sq_status run_rope_tables(double theta, int max_pos, int d, float* cos, float* s
                           cudaStream_t stream);
 }  // namespace kv
 
+namespace paged {
+// The paged KV cache (kv_paged.cu) and the attention that reads it
+// (kv_attend.cu); see the calls of the same names in sq.h.
+sq_status run_append(const void* q, const void* k, const void* v, int64_t q_stride,
+                     int64_t k_stride, int64_t v_stride, int64_t T, int hq,
+                     const sq_kv_pages& pages, const int32_t* table, int width, const int32_t* cu,
+                     const int32_t* cached, int B, const float* cos, const float* sin, int max_pos,
+                     int rot, int interleaved, const float* q_norm, const float* k_norm, float eps,
+                     void* q_out, cudaStream_t stream);
+sq_status run_dequant(const sq_kv_pages& pages, const int32_t* table, int width, const int32_t* cu,
+                      const int32_t* cached, int B, int64_t T, void* k_out, void* v_out,
+                      cudaStream_t stream);
+size_t attention_workspace_bytes(int64_t T, int hq, int hkv, int max_q, int bits);
+// prefix_table null and prefix_len 0: no shared prefix.
+sq_status run_attention(const void* q, int64_t q_stride, int64_t T, int hq,
+                        const sq_kv_pages& pages, const int32_t* prefix_table, int prefix_len,
+                        const int32_t* table, int width, const int32_t* cu, const int32_t* lengths,
+                        int B, int max_q, const sq_score_rule& rule, void* out, float* lse,
+                        void* ws, size_t ws_bytes, cudaStream_t stream);
+}  // namespace paged
+
 }  // namespace sq

@@ -1,0 +1,380 @@
+"""The paged KV cache on the GPU against the float64 oracle: append, read-back, attention over pages and
+behind a shared prefix, and the calls one after another as a server makes them."""
+import numpy as np
+import pytest
+import torch
+
+import rotation_ptq_b200 as sq
+from oracle import oracle as O
+from tests import paged as G
+from tests import parity as P
+
+pytestmark = pytest.mark.gpu
+D = 128
+STREAM_EPS = 2.0 ** -19      # weights held as two fp16 halves (2^-22) and ex2 (2^-22), sums of both
+
+
+def cu(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+def bf16(a):
+    return torch.from_numpy(np.ascontiguousarray(a, np.float64)).to(torch.bfloat16).cuda()
+
+
+def pages_of(pool):
+    return sq.KVPages(**{k: cu(v) for k, v in pool.arrays.items()})
+
+
+def attend(prob, pages=None, q=None, **kw):
+    pages = pages_of(prob.pool) if pages is None else pages
+    out = torch.full((prob.T, prob.hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((prob.T, prob.hq), 7.0, device="cuda")
+    args = dict(max_q=max(prob.new, default=1), out=out, lse=lse,
+                slopes=None if prob.slopes is None else cu(prob.slopes), **prob.rule)
+    args.update(kw)
+    q = bf16(prob.q) if q is None else q
+    batch = (cu(prob.table()), cu(prob.cu), cu(np.array(prob.own, np.int32)))
+    if prob.prefix:
+        got = sq.kv_prefix_attention(q, pages, cu(prob.prefix_table()), prob.prefix, *batch, **args)
+    else:
+        got = sq.kv_paged_attention(q, pages, *batch, **args)
+    assert got is out
+    return out, lse
+
+
+def check(prob, out, lse, eps=STREAM_EPS):
+    ref = prob.reference()
+    b_out, b_lse = prob.bounds(ref, eps)
+    o, m = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    n = sum(prob.new)
+    assert (o[n:] == 7).all() and (m[n:] == 7).all(), "rows behind the last sequence were written"
+    empty = np.isneginf(ref[1][:n])
+    assert np.array_equal(np.isneginf(m[:n]), empty)
+    assert (o[:n][empty] == 0).all()
+    err = np.abs(o[:n] - ref[0][:n])
+    assert (err <= b_out[:n]).all(), "out: %.3g times its bound" % (err / b_out[:n]).max()
+    live = ~empty
+    err = np.abs(m[:n] - np.where(live, ref[1][:n], 0))[live]
+    assert (err <= b_lse[:n][live]).all(), "lse: %.3g times its bound" % (err / b_lse[:n][live]).max()
+    assert sq.device_status() == 0
+
+
+# ------------------------------------------------------------------ append
+
+
+def append_case(seed, new, cached, hq, hkv, page, bits, rot, interleaved, norm, pad=0, strided=True):
+    rng = np.random.default_rng(seed)
+    total = [n + c for n, c in zip(new, cached)]
+    pool = G.Pool(rng, total, page, hkv, bits)
+    T = sum(new) + pad
+    qkv = rng.standard_normal((T, hq + 2 * hkv, D)) * np.exp(rng.standard_normal((T, hq + 2 * hkv, 1)))
+    qkv[:, hq:hq + hkv, ::37] *= 8
+    qkv = G.round_bf16(qkv)
+    t = bf16(qkv)
+    q, k, v = t[:, :hq], t[:, hq:hq + hkv], t[:, hq + hkv:]
+    if not strided:
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+    cos = sin = None
+    if rot:
+        ang = np.arange(max(total) + 1)[:, None] * 1e6 ** (-np.arange(0, rot, 2) / rot)
+        cos, sin = np.cos(ang).astype(np.float32), np.sin(ang).astype(np.float32)
+    w = [(1 + 0.2 * rng.standard_normal(D)).astype(np.float32) for _ in range(2)] if norm else [None, None]
+    pos = np.concatenate([c + np.arange(n) for n, c in zip(new, cached)]).astype(int)
+    seq = np.repeat(np.arange(len(new)), new)
+    return dict(pool=pool, T=T, n=sum(new), qkv=qkv, q=q, k=k, v=v, cos=cos, sin=sin, w=w, pos=pos, seq=seq,
+                cu=np.concatenate([[0], np.cumsum(new)]).astype(np.int32), cached=np.array(cached, np.int32),
+                hq=hq, hkv=hkv, bits=bits, page=page, interleaved=interleaved)
+
+
+def run_append(c, pages, **kw):
+    opt = lambda a: None if a is None else cu(a)  # noqa: E731
+    args = dict(interleaved=c["interleaved"], q_norm=opt(c["w"][0]), k_norm=opt(c["w"][1]), eps=1e-6)
+    args.update(kw)
+    return sq.kv_paged_append(c["q"], c["k"], c["v"], pages, cu(c["pool"].table), cu(c["cu"]), cu(c["cached"]),
+                              opt(c["cos"]), opt(c["sin"]), **args)
+
+
+@pytest.mark.parametrize("new,cached,hq,hkv,page,bits,rot,interleaved,norm,pad", [
+    ([1], [0], 1, 1, 16, 4, 128, False, False, 0),
+    ([1, 1, 1], [15, 16, 17], 4, 1, 16, 4, 128, False, True, 2),
+    ([5, 0, 33, 1], [0, 9, 31, 100], 8, 2, 32, 4, 64, False, True, 3),
+    ([40, 17], [3, 0], 6, 3, 16, 8, 32, True, True, 1),
+    ([9, 70], [60, 1], 7, 7, 64, 8, 96, False, False, 0),
+    ([11], [5], 10, 5, 128, 4, 112, True, False, 4),
+    ([130], [1000], 32, 8, 256, 4, 128, True, True, 0),
+    ([6, 6], [0, 2], 8, 8, 16, 8, 0, False, True, 0),
+    ([6, 6], [0, 2], 4, 2, 16, 4, 0, False, False, 0),
+    ([64], [0], 256, 64, 16, 4, 16, False, True, 0),
+])
+def test_append_and_read_back(new, cached, hq, hkv, page, bits, rot, interleaved, norm, pad):
+    c = append_case(11, new, cached, hq, hkv, page, bits, rot, interleaved, norm, pad)
+    pages = pages_of(c["pool"])
+    before = {k: getattr(pages, k).clone() for k in c["pool"].arrays}
+    q_out = torch.full((c["T"], hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert run_append(c, pages, q_out=q_out) is q_out
+    n, x = c["n"], c["qkv"][:c["n"]]
+    # queries: float32 norm, rotary map and butterflies.  Each of the 128 terms of an output takes part in
+    # at most 14 float32 operations, each off by 2^-24 of the vector's 1-norm / sqrt(128); then bf16
+    ref = O.head_forward(x[:, :hq], c["w"][0], 1e-6, c["pos"], c["cos"], c["sin"], interleaved)
+    got = q_out.double().cpu().numpy()
+    size = np.abs(O.rope_part(O.rms_norm(x[:, :hq], c["w"][0], 1e-6), c["pos"], None, None, False)).sum(-1, keepdims=True)
+    bound = 2.0 ** -8 * np.abs(ref) + 14 * 2.0 ** -24 * 2 * size / np.sqrt(D) + 1e-30
+    assert (np.abs(got[:n] - ref) <= bound).all()
+    assert (got[n:] == 7).all()
+    # caches: the exact rotation rounded once to float32, then the contiguous caches' rule
+    k = O.head_forward(x[:, hq:hq + hkv], c["w"][1], 1e-6, c["pos"], c["cos"], c["sin"], interleaved).astype(np.float32)
+    page_of, row = c["pool"].table[c["seq"], c["pos"] // page], c["pos"] % page
+    touched = np.zeros((pages.num_pages, page), bool)
+    touched[page_of, row] = True
+    back = sq.kv_paged_dequant(pages, cu(c["pool"].table), cu(c["cu"]), cu(c["cached"]), c["T"],
+                               k_out=torch.full((c["T"], hkv, D), 7.0, dtype=torch.bfloat16, device="cuda"),
+                               v_out=torch.full((c["T"], hkv, D), 7.0, dtype=torch.bfloat16, device="cuda"))
+    for key, val, rb in (("k", k, back[0]), ("v", x[:, hq + hkv:].astype(np.float32), back[1])):
+        codes, scale, zero, v = G.quantize(val, bits)
+        raw = getattr(pages, key + "_codes").cpu().numpy()[page_of, :, row]
+        mine = O.unpack_int4(raw, signed=False) if bits == 4 else raw
+        P.check_codes(mine, codes, v, key)
+        got_s = getattr(pages, key + "_scale").cpu().numpy()[page_of, :, row]
+        got_z = getattr(pages, key + "_zero").cpu().numpy()[page_of, :, row]
+        P.check_scales(got_s, scale)
+        assert np.array_equal(got_z, zero)
+        # read-back: one float32 product of exact factors, then bf16: the exact rounding but at double ties
+        want = torch.from_numpy((mine.astype(np.float32) - got_z[..., None].astype(np.float32)) * got_s[..., None])
+        assert torch.equal(rb[:n].cpu(), want.to(torch.bfloat16))
+        assert (rb[n:] == 7).all()
+        # nothing else in the pool moved
+        for part in ("_codes", "_scale", "_zero"):
+            a, b = getattr(pages, key + part).cpu().numpy(), before[key + part].cpu().numpy()
+            keep = ~np.broadcast_to(touched[:, None, :], a.shape[:3])
+            assert np.array_equal(a[keep], b[keep], equal_nan=part == "_scale")
+    assert sq.device_status() == 0
+
+
+def test_append_matches_the_contiguous_cache():
+    """Without a norm and with the whole head rotated, the codes are those of kv_rotate_quant, bit for bit."""
+    c = append_case(12, [200], [0], 32, 8, 64, 4, 128, False, False, strided=False)
+    pages = pages_of(c["pool"])
+    q_out = run_append(c, pages)
+    ref = sq.kv_rotate_quant(c["q"], c["k"], c["v"], cu(c["pos"].astype(np.int32)), cu(c["cos"]), cu(c["sin"]))
+    t, r = c["pool"].table[0, c["pos"] // 64], c["pos"] % 64
+    for key in ("k", "v"):
+        assert torch.equal(getattr(pages, key + "_codes")[t, :, r], ref[key + "_cache"])
+        assert torch.equal(getattr(pages, key + "_scale")[t, :, r], ref[key + "_scale"])
+        assert torch.equal(getattr(pages, key + "_zero")[t, :, r], ref[key + "_zero"])
+    assert torch.allclose(q_out.float(), ref["q_out"].float(), rtol=2.0 ** -7, atol=2.0 ** -16)
+
+
+def test_append_reports_what_is_out_of_range():
+    c = append_case(13, [4, 4, 4], [0, 0, 0], 4, 2, 16, 4, 128, False, False)
+    pages = pages_of(c["pool"])
+    ok = {k: v.copy() for k, v in (("table", c["pool"].table), ("cu", c["cu"]), ("cached", c["cached"]))}
+
+    def call(**bad):
+        a = {**ok, **bad}
+        q_out = torch.full((c["T"], 4, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        sq.kv_paged_append(c["q"], c["k"], c["v"], pages, cu(a["table"]), cu(a["cu"]), cu(a["cached"]),
+                           cu(c["cos"]), cu(c["sin"]), q_out=q_out)
+        assert sq.device_status() == 1          # SQ_ERR_INVALID_ARG
+        return (q_out == 7).all(-1).all(-1).cpu().numpy()
+
+    table = ok["table"].copy()
+    table[1, 0] = pages.num_pages
+    assert call(table=table).tolist() == [False] * 4 + [True] * 4 + [False] * 4
+    table[1, 0] = -1
+    assert call(table=table).tolist() == [False] * 4 + [True] * 4 + [False] * 4
+    assert call(cached=np.array([0, -3, 0], np.int32)).tolist() == [False] * 4 + [True] * 4 + [False] * 4
+    width = 16 * ok["table"].shape[1]
+    got = call(cached=np.array([0, width - 2, 0], np.int32), table=np.zeros_like(ok["table"]))
+    assert got.tolist() == [False] * 4 + [True] * 4 + [False] * 4      # positions behind the rope tables
+    got = call(cu=np.array([0, 4, 3, 12], np.int32))
+    assert got[:3].tolist() == [False] * 3
+
+
+# --------------------------------------------------------------- attention
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("new,own,hq,hkv,page", [
+    ([1], [1], 4, 1, 16),
+    ([1], [16], 1, 1, 16),
+    ([1, 1, 1, 1], [17, 64, 65, 300], 8, 2, 16),
+    ([1] * 9, [1, 2, 15, 31, 33, 63, 127, 128, 129], 32, 8, 32),
+    ([1, 1], [1500, 700], 14, 2, 64),               # 7 query heads per KV head
+    ([1, 1], [333, 90], 16, 1, 16),                 # 16
+    ([1], [200], 48, 1, 256),                       # more rows than one block
+    ([2, 0, 3, 1], [2, 40, 100, 7], 8, 2, 16),      # drafts beside an idle sequence
+    ([5, 8], [5, 400], 4, 4, 32),
+    ([40, 17], [40, 90], 8, 2, 16),                 # whole prompts and chunks
+    ([3, 2], [1, 0], 4, 2, 16),                     # fewer cached tokens than new ones: empty rows
+])
+def test_attention(new, own, hq, hkv, page, bits):
+    prob = G.Attention(21, new, own, hq, hkv, page, bits, pad=2)
+    check(prob, *attend(prob))
+
+
+@pytest.mark.parametrize("rule", [
+    dict(softcap=20.0), dict(softcap=0.5), dict(window=1), dict(window=33), dict(slopes=True),
+    dict(scale=0.31), dict(scale=-0.1), dict(scale=0.0), dict(softcap=30.0, window=70, slopes=True),
+    dict(window=1 << 30)])
+@pytest.mark.parametrize("prefix", [0, 45])
+def test_score_rules(rule, prefix):
+    prob = G.Attention(22, [1, 4, 20], [150, 81, 20], 8, 2, 16, 4, prefix=prefix, pad=1, **rule)
+    check(prob, *attend(prob))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("prefix,new,own,hq,hkv,page", [
+    (1, [1], [1], 4, 1, 16),
+    (64, [1, 1], [0, 5], 8, 2, 16),                 # a sequence with nothing of its own but the prefix
+    (129, [1] * 7, [1, 2, 3, 16, 17, 64, 65], 32, 8, 32),
+    (700, [2, 5, 1], [2, 30, 200], 14, 2, 64),
+    (50, [30, 3], [30, 100], 8, 2, 16),
+])
+def test_prefix(prefix, new, own, hq, hkv, page, bits):
+    prob = G.Attention(23, new, own, hq, hkv, page, bits, prefix=prefix, pad=1)
+    check(prob, *attend(prob))
+
+
+@pytest.mark.parametrize("kw", [dict(k_size=30.0, q_size=4.0), dict(k_size=1e-3, q_size=1e-3),
+                                dict(v_size=1e4), dict(v_size=1e-6), dict(q_size=1e4, k_size=1e-4)])
+def test_sizes_of_values(kw):
+    prob = G.Attention(24, [1, 3], [400, 77], 8, 2, 16, 4, **kw)
+    check(prob, *attend(prob))
+
+
+def test_long_cache_splits_and_is_repeatable():
+    prob = G.Attention(25, [1, 1], [9000, 5], 4, 1, 128, 4)
+    a = attend(prob)
+    check(prob, *a)
+    b = attend(prob)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    # unsplit (no workspace worth the name): the same but for the order of sums
+    c = attend(prob, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+    check(prob, *c)
+
+
+def test_strided_queries_and_other_stream():
+    prob = G.Attention(26, [1, 2], [100, 60], 8, 2, 16, 4)
+    wide = torch.zeros((prob.T, 12, D), dtype=torch.bfloat16, device="cuda")
+    wide[:, 2:10] = bf16(prob.q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = attend(prob, q=wide[:, 2:10])
+    side.synchronize()
+    check(prob, *got)
+
+
+def test_hidden_infinities_do_not_leak():
+    """A later key's infinite or NaN scale is no business of earlier rows."""
+    prob = G.Attention(27, [6], [80], 4, 1, 16, 4)
+    ref = prob.reference()
+    pages = pages_of(prob.pool)
+    page, row = prob.table()[0, 79 // 16], 79 % 16
+    for bad, keys in ((float("inf"), "kv"), (float("nan"), "kv"), (float("nan"), "v"), (float("inf"), "v")):
+        for key in "kv":
+            getattr(pages, key + "_scale")[page, :, row] = bad if key in keys else 0.5
+        out, lse = attend(prob, pages)
+        b_out, b_lse = prob.bounds(ref, STREAM_EPS)
+        o, m = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        assert (np.abs(o[:5] - ref[0][:5]) <= b_out[:5]).all()
+        assert (np.abs(m[:5] - ref[1][:5]) <= b_lse[:5]).all()
+        if keys == "v":                                # a visible key's scale, under finite scores
+            assert not np.isfinite(o[5]).any()
+
+
+def test_attention_reports_what_is_out_of_range():
+    prob = G.Attention(28, [1, 1, 1], [20, 30, 40], 4, 2, 16, 4)
+    pages, q = pages_of(prob.pool), bf16(prob.q)
+    good = attend(prob, pages)[0]
+
+    def call(table=None, cu_=None, lengths=None):
+        out = torch.full((3, 4, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        sq.kv_paged_attention(q, pages, cu(prob.table() if table is None else table),
+                              cu(prob.cu if cu_ is None else cu_),
+                              cu(np.array(prob.own if lengths is None else lengths, np.int32)), 1, out=out)
+        assert sq.device_status() == 1
+        return out
+
+    for bad in (-1, 16 * prob.table().shape[1] + 1):
+        out = call(lengths=[20, bad, 40])
+        assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2]) and (out[1] == 0).all()
+    table = prob.table().copy()
+    table[1, :] = -1
+    out = call(table=table)
+    assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2]) and (out[1] == 0).all()
+    out = call(cu_=np.array([0, 1, 2, 9], np.int32))                  # rows behind the batch
+    assert torch.equal(out[:2], good[:2]) and (out[2] == 7).all()
+
+
+def test_two_graphs_replay_side_by_side():
+    """Captured calls carry their own workspaces; lengths are read at replay."""
+    probs = [G.Attention(29, [1, 1], [3000, 20], 4, 1, 64, 4), G.Attention(30, [1], [2500], 4, 1, 64, 8)]
+    eager, graphs, held = [], [], []
+    for p in probs:
+        pages, q = pages_of(p.pool), bf16(p.q)
+        args = (cu(p.table()), cu(p.cu), cu(np.array(p.own, np.int32)), 1)
+        eager.append(sq.kv_paged_attention(q, pages, *args).clone())
+        out = torch.empty_like(q)
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            sq.kv_paged_attention(q, pages, *args, out=out)
+        graphs.append((g, out))
+        held.append((pages, q, args))
+    streams = [torch.cuda.Stream() for _ in probs]
+    for _ in range(20):
+        for (g, out), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                out.zero_()
+                g.replay()
+    torch.cuda.synchronize()
+    for (g, out), e in zip(graphs, eager):
+        assert torch.equal(out, e)
+    # a shorter sequence at the next replay
+    held[0][2][2][0] = 1000
+    graphs[0][0].replay()
+    torch.cuda.synchronize()
+    want = sq.kv_paged_attention(held[0][1], held[0][0], *held[0][2])
+    assert torch.equal(graphs[0][1], want)
+
+
+# --------------------------------------------------- the calls one after another
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_prompt_then_steps(bits):
+    """A prompt in two chunks, then single tokens: every call's attention equals the oracle's over what the
+    cache then holds, and the whole cache reads back."""
+    rng = np.random.default_rng(31)
+    hq, hkv, page, lens = 8, 2, 16, [37, 20]
+    B, longest = 2, 64
+    pages = sq.KVPages.empty(12, page, hkv, bits)
+    table = rng.permutation(12)[:B * 4].reshape(B, 4).astype(np.int32)
+    ang = np.arange(longest)[:, None] * 1e4 ** (-np.arange(0, D, 2) / D)
+    cos, sin = np.cos(ang).astype(np.float32), np.sin(ang).astype(np.float32)
+    w = (1 + 0.1 * rng.standard_normal(D)).astype(np.float32)
+    cached = np.zeros(B, np.int32)
+    for new in ([30, 20], [7, 0], [1, 1], [1, 1]):
+        T = sum(new)
+        x = G.round_bf16(rng.standard_normal((T, hq + 2 * hkv, D)))
+        t = bf16(x)
+        c = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        q = sq.kv_paged_append(t[:, :hq], t[:, hq:hq + hkv], t[:, hq + hkv:], pages, cu(table), cu(c), cu(cached),
+                               cu(cos), cu(sin), q_norm=cu(w), k_norm=cu(w))
+        cached = (cached + np.array(new)).astype(np.int32)
+        out = sq.kv_paged_attention(q, pages, cu(table), cu(c), cu(cached), max(new))
+        whole = np.concatenate([[0], np.cumsum(cached)]).astype(np.int32)
+        k, v = sq.kv_paged_dequant(pages, cu(table), cu(whole), cu(np.zeros(B, np.int32)), int(cached.sum()))
+        k, v, qn = (a.double().cpu().numpy() for a in (k, v, q))
+        for b in range(B):
+            rows, own = slice(c[b], c[b + 1]), slice(whole[b], whole[b + 1])
+            ref, _, spread, size = O.causal_attention(qn[rows], k[own], v[own],
+                                                   np.arange(cached[b] - new[b], cached[b]), np.arange(cached[b]))
+            # the read-back rounds keys and values to bf16, by 2^-8 of each: a score moves by 2^-8 size at
+            # most, a weight by that part of itself, and the output's quotient by twice that and 2^-8
+            err = np.abs(out[rows].double().cpu().numpy() - ref)
+            assert (err <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -8 * (2 * size + 1) * spread).all()
+    assert cached.tolist() == [39, 22] and sq.device_status() == 0
