@@ -649,8 +649,11 @@ typedef struct {
  *            finishes; one call at a time per workspace.  With less (or NULL)
  *            the keys of a row are not split across CTAs: the same result but
  *            for the order of float32 sums, and slower.
- * Shape rules: as sq_kv_paged_append; table_width * page_size < 2^30. */
-size_t sq_kv_attention_workspace_bytes(int64_t T, int hq, int max_q, const sq_kv_pages* pages);
+ * Shape rules: as sq_kv_paged_append; table_width * page_size < 2^30,
+ * T * hq < 2^31.  (The workspace's size goes with all sizes of the call;
+ * prefix_len is 0 for sq_kv_paged_attention.) */
+size_t sq_kv_attention_workspace_bytes(int64_t T, int hq, const sq_kv_pages* pages, int B,
+                                       int table_width, int max_q, int64_t prefix_len);
 sq_status sq_kv_paged_attention(const void* q, int64_t q_stride, int64_t T, int hq,
                                 const sq_kv_pages* pages, const int32_t* block_table,
                                 int table_width, const int32_t* cu_seqlens,

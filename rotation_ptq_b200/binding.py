@@ -108,7 +108,7 @@ lib.sq_kv_paged_append.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32, 
 lib.sq_kv_paged_dequant.restype = _i32
 lib.sq_kv_paged_dequant.argtypes = [_vp, _vp, _i32, _vp, _vp, _i32, _i64, _vp, _vp, _vp]
 lib.sq_kv_attention_workspace_bytes.restype = ctypes.c_size_t
-lib.sq_kv_attention_workspace_bytes.argtypes = [_i64, _i32, _i32, _vp]
+lib.sq_kv_attention_workspace_bytes.argtypes = [_i64, _i32, _vp, _i32, _i32, _i32, _i64]
 lib.sq_kv_paged_attention.restype = _i32
 lib.sq_kv_paged_attention.argtypes = [_vp, _i64, _i64, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _i32,
                                       _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
@@ -643,7 +643,6 @@ class KVPages:
         self._struct = _PagesStruct(*(t.data_ptr() for t in self._tensors), n, ps, hkv, 128,
                                     self.bits)
         self._ref = ctypes.addressof(self._struct)
-        self._ws_bytes = {}
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, hkv: int, bits: int = 4, device=None):
@@ -780,9 +779,12 @@ def kv_paged_dequant(pages: KVPages, block_table: torch.Tensor, cu_seqlens: torc
     return k_out, v_out
 
 
-def kv_attention_workspace_bytes(T: int, hq: int, max_q: int, pages: KVPages) -> int:
-    """Scratch bytes that let the paged attention calls split keys across CTAs."""
-    return int(lib.sq_kv_attention_workspace_bytes(int(T), int(hq), int(max_q), pages._ref))
+def kv_attention_workspace_bytes(T: int, hq: int, pages: KVPages, B: int, table_width: int,
+                                 max_q: int, prefix_len: int = 0) -> int:
+    """Scratch bytes that let the paged attention calls split keys across CTAs
+    (and read a shared prefix once)."""
+    return int(lib.sq_kv_attention_workspace_bytes(int(T), int(hq), pages._ref, int(B),
+                                                   int(table_width), int(max_q), int(prefix_len)))
 
 
 def kv_paged_attention(q: torch.Tensor, pages: KVPages, block_table: torch.Tensor,
@@ -868,10 +870,7 @@ def _kv_attention(q, pages, prefix_table, prefix_len, block_table, cu_seqlens, l
     with _on_device(q.device):
         stream = _stream(q)
         if workspace is None:
-            key = (T, hq, max_q)
-            need = pages._ws_bytes.get(key)
-            if need is None:
-                need = pages._ws_bytes[key] = kv_attention_workspace_bytes(T, hq, max_q, pages)
+            need = kv_attention_workspace_bytes(T, hq, pages, B, width, max_q, prefix_len)
             workspace = _attention_workspace(q.device, stream, need) if need else None
         ws_ptr = None if workspace is None else workspace.data_ptr()
         ws_bytes = 0 if workspace is None else workspace.numel()

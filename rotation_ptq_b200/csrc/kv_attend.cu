@@ -61,25 +61,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
-// Four fp16 pairs (nibble i, nibble i + 4), i = 0..3, of a word of 8 codes,
-// less the zero points z (lo half: the pair's first, hi half: its second).
-// 0x6400 | n is 1024 + n, and 0x6400 | 16 n is 1024 + 16 n: one fma by 1/16
-// takes the place of a shift.  All steps are exact.
-__device__ __forceinline__ void widen_nibbles(uint32_t w, __half2 z1, __half2 z16, uint32_t (&o)[4]) {
-  const __half2 sixteenth = __float2half2_rn(0.0625f);
-  const uint32_t w8 = w >> 8;
-  o[0] = h2_bits(__hadd2(bits_h2((w & 0x000F000Fu) | 0x64006400u), z1));
-  o[1] = h2_bits(__hfma2(bits_h2((w & 0x00F000F0u) | 0x64006400u), sixteenth, z16));
-  o[2] = h2_bits(__hadd2(bits_h2((w8 & 0x000F000Fu) | 0x64006400u), z1));
-  o[3] = h2_bits(__hfma2(bits_h2((w8 & 0x00F000F0u) | 0x64006400u), sixteenth, z16));
-}
-
-// Two fp16 pairs (bytes 0, 1) and (2, 3) of a word of 4 codes, less z.
-__device__ __forceinline__ void widen_bytes(uint32_t w, __half2 z1, uint32_t (&o)[2]) {
-  o[0] = h2_bits(__hadd2(bits_h2(__byte_perm(w, 0x64646464u, 0x4140u)), z1));
-  o[1] = h2_bits(__hadd2(bits_h2(__byte_perm(w, 0x64646464u, 0x4342u)), z1));
-}
-
 template <int BITS>
 struct KFrag {                             // a lane's codes of one key row: 32
   uint4 c[BITS / 4];
@@ -169,7 +150,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 3) stream_kernel(const 
 
   // ---- the list: this CTA's piece, and the sequence it begins in
   auto weight = [&](const Seq& s, int& per) {
-    const int nrt = (s.qlen * G + R - 1) / R;
+    const int nrt = s.qlen * G > P.many_rows ? 0 : (s.qlen * G + R - 1) / R;
     per = split ? max(s.tiles(), 1) : 1;   // tiles per unit; a unit without keys still writes zeros
     return static_cast<int64_t>(nrt) * hkv * per;
   };
@@ -543,6 +524,18 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 3) stream_kernel(const 
         if (r < u.rows) {
           const int tok = (u.row0 + r) / G, head = u.h * G + u.row0 + r - tok * G;
           const int64_t row = static_cast<int64_t>(u.s.row0 + tok) * P.hq + head;
+          // the shared prefix's part of the row, in pieces
+          for (int e = 0; e < P.ex_n; ++e) {
+            const int64_t at = static_cast<int64_t>(e) * P.batch.T * P.hq + row;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(P.ex_ml) + at);
+            const float po = __ldcg(P.ex_o + at * D + tid);
+            const float M = fmaxf(mm[r], ml.x);
+            const float fa = mm[r] == -INFINITY ? 0.f : ex2(mm[r] - M);
+            const float fb = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+            acc[r] = fa * acc[r] + (fb != 0.f ? fb * po : 0.f);
+            ll[r] = fa * ll[r] + fb * ml.y;
+            mm[r] = M;
+          }
           const float y = ll[r] == 0.f ? 0.f : acc[r] / ll[r];
           P.out[row * D + tid] = __float2bfloat16_rn(y);
           if (P.lse && tid == r) P.lse[row] = ll[r] == 0.f ? -INFINITY : (mm[r] + log2f(ll[r])) * kLn2;
@@ -582,16 +575,59 @@ int any_grid(int bits, int nt) {
   return nt == 1 ? grid_size<8, 1>() : grid_size<8, 2>();
 }
 
-// Rows per unit: 8 when a sequence's rows fit, else 16.
-int choose_nt(int G, int max_q) { return static_cast<int64_t>(G) * max_q <= 8 ? 1 : 2; }
+// Sequences of up to this many rows (new tokens x query heads per KV head)
+// go to the streaming kernel, longer ones to the tile kernel.
+constexpr int kFewRows = 16;
+// A shared prefix is read once for the batch while no sequence has more rows
+// than this; longer ones fill the tile kernel's rows by themselves.
+constexpr int kSharedRows = 128;
+constexpr int kTileRows = 256;
+constexpr size_t kPartFloats = static_cast<size_t>(kTileRows) * (D + 2);
 
+AttnPlan make_plan(int64_t T, int hq, int hkv, int B, int max_q, int64_t keys, int prefix_len,
+                   int bits, bool have_ws) {
+  AttnPlan p{};
+  const int64_t G = hq / hkv, rows = G * max_q;
+  const int sms = host::num_sms();
+  p.nt = rows <= 8 ? 1 : 2;
+  p.shared = prefix_len > 0 && rows <= kSharedRows && B > 1 && have_ws;
+  p.tile = !p.shared && rows > kFewRows;
+  p.stream = p.shared || !p.tile || B > 1;
+  p.tile_split = 1;
+  size_t at = 2 * kCountBytes;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  if (p.stream)
+    p.part = take(static_cast<size_t>(any_grid(bits, p.nt)) * 2 * (8 * p.nt) * (D + 2) * 4);
+  if (p.shared) {
+    const int64_t units = (T * G + kTileRows - 1) / kTileRows * hkv, tiles = (prefix_len + 127) / 128;
+    int64_t s = sms / units;
+    if (s > (tiles + 1) / 2) s = (tiles + 1) / 2;
+    p.tile_split = static_cast<int>(s < 1 ? 1 : s);
+    p.tile_units = units * p.tile_split;
+    p.ex_o = take(static_cast<size_t>(p.tile_split) * T * hq * D * 4);
+    p.ex_ml = take(static_cast<size_t>(p.tile_split) * T * hq * 2 * 4);
+  } else if (p.tile) {
+    const int64_t slots = (T * G / kTileRows + B) * hkv, tiles = (keys + prefix_len + 127) / 128;
+    int64_t s = have_ws ? 2 * sms / slots : 1;
+    if (s > (tiles + 1) / 2) s = (tiles + 1) / 2;
+    if (s < 1 || slots > static_cast<int64_t>(kCountBytes / 4)) s = 1;
+    p.tile_split = static_cast<int>(s);
+    p.tile_units = slots * s;
+    if (s > 1) p.tpart = take(static_cast<size_t>(slots) * s * kPartFloats * 4);
+  }
+  p.bytes = at;
+  return p;
+}
 
 }  // namespace
 
-size_t attention_workspace_bytes(int64_t T, int hq, int hkv, int max_q, int bits) {
-  (void)T;
-  const int nt = choose_nt(hq / hkv, max_q), grid = any_grid(bits, nt);
-  return kCountBytes + static_cast<size_t>(grid) * 2 * (8 * nt) * (D + 2) * 4;
+size_t attention_workspace_bytes(int64_t T, int hq, int hkv, int B, int max_q, int64_t keys,
+                                 int prefix_len, int bits) {
+  return make_plan(T, hq, hkv, B, max_q, keys, prefix_len, bits, true).bytes;
 }
 
 sq_status run_attention(const void* q, int64_t q_stride, int64_t T, int hq,
@@ -599,7 +635,7 @@ sq_status run_attention(const void* q, int64_t q_stride, int64_t T, int hq,
                         const int32_t* table, int width, const int32_t* cu, const int32_t* lengths,
                         int B, int max_q, const sq_score_rule& rule, void* out, float* lse,
                         void* ws, size_t ws_bytes, cudaStream_t stream) {
-  AttnParams P;
+  AttnParams P{};
   P.q = static_cast<const __nv_bfloat16*>(q);
   P.sq = q_stride;
   P.pages = Pages{pages.k_codes, pages.k_scale, pages.k_zero, pages.v_codes, pages.v_scale,
@@ -616,16 +652,39 @@ sq_status run_attention(const void* q, int64_t q_stride, int64_t T, int hq,
   P.slopes = rule.slopes;
   P.out = static_cast<__nv_bfloat16*>(out);
   P.lse = lse;
-  const int nt = choose_nt(P.G, max_q), grid = any_grid(pages.bits, nt);
-  const size_t need = attention_workspace_bytes(T, hq, pages.hkv, max_q, pages.bits);
-  const bool split = ws && ws_bytes >= need;
-  P.count = split ? static_cast<unsigned*>(ws) : nullptr;
-  P.part = split ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCountBytes) : nullptr;
-  auto kern = pages.bits == 4 ? (nt == 1 ? stream_kernel<4, 1> : stream_kernel<4, 2>)
-                              : (nt == 1 ? stream_kernel<8, 1> : stream_kernel<8, 2>);
+  P.spin_limit = host::spin_limit();
+  const int64_t keys = static_cast<int64_t>(width) * pages.page_size;
+  AttnPlan plan = make_plan(T, hq, pages.hkv, B, max_q, keys, prefix_len, pages.bits, true);
+  const bool have = ws && ws_bytes >= plan.bytes;
+  if (!have) plan = make_plan(T, hq, pages.hkv, B, max_q, keys, prefix_len, pages.bits, false);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  P.many_rows = plan.tile ? kFewRows : 0x7fffffff;
+  P.few_rows = plan.stream ? kFewRows : 0;
+  P.shared = plan.shared;
+  P.nsplit = plan.tile_split;
+  P.units = plan.tile_units;
+  if (have) {
+    P.count = reinterpret_cast<unsigned*>(base);
+    P.tcount = reinterpret_cast<unsigned*>(base + kCountBytes);
+    P.part = reinterpret_cast<float*>(base + plan.part);
+    P.tpart = reinterpret_cast<float*>(base + plan.tpart);
+  }
+  if (plan.shared) {
+    P.ex_o = reinterpret_cast<float*>(base + plan.ex_o);
+    P.ex_ml = reinterpret_cast<float*>(base + plan.ex_ml);
+  }
+  if (plan.tile || plan.shared) {
+    const sq_status st = launch_tile(P, pages.bits, stream);
+    if (st != SQ_OK) return st;
+  }
+  if (!plan.stream) return SQ_OK;
+  P.ex_n = plan.shared ? plan.tile_split : 0;
+  const int grid = any_grid(pages.bits, plan.nt);
+  auto kern = pages.bits == 4 ? (plan.nt == 1 ? stream_kernel<4, 1> : stream_kernel<4, 2>)
+                              : (plan.nt == 1 ? stream_kernel<8, 1> : stream_kernel<8, 2>);
   kern<<<grid, THREADS, 0, stream>>>(P);
   cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? SQ_OK : host::cuda_fail("kv_paged_attention launch", e);
+  return e == cudaSuccess ? SQ_OK : host::cuda_fail("kv attention launch", e);
 }
 
 }  // namespace paged

@@ -29,8 +29,20 @@ struct AttnParams {
   const float* slopes;                     // [hq], or null
   __nv_bfloat16* out;                      // [T][hq][128]
   float* lse;                              // [T][hq], or null
+  uint32_t spin_limit;
+  // the streaming kernel: sequences of up to many_rows rows (others are the tile kernel's)
+  int many_rows;
   unsigned* count;                         // workspace, zero at rest: one counter per CTA
   float* part;                             // null: units are not split
+  // the tile kernel: sequences of more than few_rows rows, or all rows over the prefix (shared)
+  int few_rows, shared, nsplit;
+  int64_t units;
+  unsigned* tcount;                        // workspace, zero at rest: one counter per unit
+  float* tpart;                            // [units / nsplit][nsplit]: O [256][128], (m, l) [256]
+  // the shared prefix's partial results, for the streaming kernel to join
+  int ex_n;                                // pieces, 0: none
+  float* ex_o;                             // [piece][T][hq][128]
+  float* ex_ml;                            // [piece][T][hq][2]
 };
 
 // One sequence's new tokens and keys.  Positions count the shared prefix
@@ -40,6 +52,7 @@ struct Seq {
   int row0, qlen, len;                     // first packed row; new tokens; own cached tokens
   int pos0;                                // position of the first new token (may be negative)
   int pt0, pn, ot0, on;                    // first tile and tile count: prefix, own
+  bool keys;                               // its lengths make sense
   __device__ __forceinline__ int tiles() const { return pn + on; }
 };
 
@@ -61,12 +74,15 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& P, int b, bool report)
     if (report) record_status(SQ_ERR_INVALID_ARG);
     s.len = 0;
   }
+  s.keys = keys;
   s.pos0 = P.prefix_len + s.len - s.qlen;
   int low = 0;                             // lowest visible position of any new token
   if (P.window > 0 && s.pos0 - P.window + 1 > 0) low = s.pos0 - P.window + 1;
   const int own_low = low > P.prefix_len ? low - P.prefix_len : 0;
   s.pt0 = low / TILE;
-  s.pn = keys && s.qlen > 0 && low < P.prefix_len ? (P.prefix_len - 1) / TILE - s.pt0 + 1 : 0;
+  s.pn = keys && s.qlen > 0 && low < P.prefix_len && P.ex_n == 0
+             ? (P.prefix_len - 1) / TILE - s.pt0 + 1
+             : 0;
   s.ot0 = own_low / TILE;
   s.on = keys && s.qlen > 0 && own_low < s.len ? (s.len - 1) / TILE - s.ot0 + 1 : 0;
   return s;
@@ -90,6 +106,36 @@ __device__ __forceinline__ float ex2(float x) {
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+
+// Four fp16 pairs (nibble i, nibble i + 4), i = 0..3, of a word of 8 codes,
+// less the zero points z (lo half: the pair's first, hi half: its second).
+// 0x6400 | n is 1024 + n, and 0x6400 | 16 n is 1024 + 16 n: one fma by 1/16
+// takes the place of a shift.  All steps are exact.
+__device__ __forceinline__ void widen_nibbles(uint32_t w, __half2 z1, __half2 z16, uint32_t (&o)[4]) {
+  const __half2 sixteenth = __float2half2_rn(0.0625f);
+  const uint32_t w8 = w >> 8;
+  o[0] = h2_bits(__hadd2(bits_h2((w & 0x000F000Fu) | 0x64006400u), z1));
+  o[1] = h2_bits(__hfma2(bits_h2((w & 0x00F000F0u) | 0x64006400u), sixteenth, z16));
+  o[2] = h2_bits(__hadd2(bits_h2((w8 & 0x000F000Fu) | 0x64006400u), z1));
+  o[3] = h2_bits(__hfma2(bits_h2((w8 & 0x00F000F0u) | 0x64006400u), sixteenth, z16));
+}
+
+// Two fp16 pairs (bytes 0, 1) and (2, 3) of a word of 4 codes, less z.
+__device__ __forceinline__ void widen_bytes(uint32_t w, __half2 z1, uint32_t (&o)[2]) {
+  o[0] = h2_bits(__hadd2(bits_h2(__byte_perm(w, 0x64646464u, 0x4140u)), z1));
+  o[1] = h2_bits(__hadd2(bits_h2(__byte_perm(w, 0x64646464u, 0x4342u)), z1));
+}
+
+// What a call launches and the workspace it wants (kv_attend.cu).
+struct AttnPlan {
+  int nt;                                  // streaming kernel: 8-row blocks per unit
+  bool stream, tile, shared;               // which kernels run; shared: the prefix pass
+  int tile_split;                          // CTAs that may share a tile unit
+  int64_t tile_units;
+  size_t part, tpart, ex_o, ex_ml, bytes;  // offsets in the workspace, and its size
+};
+
+sq_status launch_tile(const AttnParams& P, int bits, cudaStream_t stream);
 
 }  // namespace paged
 }  // namespace sq

@@ -428,10 +428,16 @@ sq_status sq_kv_paged_dequant(const sq_kv_pages* pages, const int32_t* block_tab
                                 v_out, static_cast<cudaStream_t>(stream));
 }
 
-size_t sq_kv_attention_workspace_bytes(int64_t T, int hq, int max_q, const sq_kv_pages* pages) {
-  if (check_pages(pages, hq) != SQ_OK || T <= 0 || max_q <= 0) return 0;
+size_t sq_kv_attention_workspace_bytes(int64_t T, int hq, const sq_kv_pages* pages, int B,
+                                       int table_width, int max_q, int64_t prefix_len) {
+  if (check_pages(pages, hq) != SQ_OK || check_batch(pages, T, B, table_width) != SQ_OK ||
+      T * hq > 0x7fffffffLL || T == 0 || B == 0 || max_q <= 0 || prefix_len < 0 ||
+      prefix_len >= (1LL << 30))
+    return 0;
   if (sq::host::current_device() < 0) return 0;
-  return sq::paged::attention_workspace_bytes(T, hq, pages->hkv, max_q, pages->bits);
+  return sq::paged::attention_workspace_bytes(
+      T, hq, pages->hkv, B, max_q, static_cast<int64_t>(table_width) * pages->page_size,
+      static_cast<int>(prefix_len), pages->bits);
 }
 
 static sq_status paged_attention(const void* q, int64_t q_stride, int64_t T, int hq,
@@ -457,6 +463,10 @@ static sq_status paged_attention(const void* q, int64_t q_stride, int64_t T, int
   if (!stride_ok(q_stride, hq)) {
     set_error("unsupported token stride %lld (need a multiple of 8 that holds the heads)",
               (long long)q_stride);
+    return SQ_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (T * hq > 0x7fffffffLL) {
+    set_error("unsupported sizes T=%lld hq=%d (need T * hq < 2^31)", (long long)T, hq);
     return SQ_ERR_UNSUPPORTED_SHAPE;
   }
   if (T == 0 || B == 0 || max_q == 0) return SQ_OK;

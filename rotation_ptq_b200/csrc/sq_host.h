@@ -150,7 +150,9 @@ sq_status run_append(const void* q, const void* k, const void* v, int64_t q_stri
 sq_status run_dequant(const sq_kv_pages& pages, const int32_t* table, int width, const int32_t* cu,
                       const int32_t* cached, int B, int64_t T, void* k_out, void* v_out,
                       cudaStream_t stream);
-size_t attention_workspace_bytes(int64_t T, int hq, int hkv, int max_q, int bits);
+// keys: rows that a sequence's table can address.
+size_t attention_workspace_bytes(int64_t T, int hq, int hkv, int B, int max_q, int64_t keys,
+                                 int prefix_len, int bits);
 // prefix_table null and prefix_len 0: no shared prefix.
 sq_status run_attention(const void* q, int64_t q_stride, int64_t T, int hq,
                         const sq_kv_pages& pages, const int32_t* prefix_table, int prefix_len,

@@ -12,6 +12,8 @@ from tests import parity as P
 pytestmark = pytest.mark.gpu
 D = 128
 STREAM_EPS = 2.0 ** -19      # weights held as two fp16 halves (2^-22) and ex2 (2^-22), sums of both
+# the tile kernel holds weights (times the value's scale) in one fp16 number: half a step is 2^-11 of it
+TILE_EPS = 2.0 ** -11 + STREAM_EPS
 
 
 def cu(a, dtype=None):
@@ -44,8 +46,15 @@ def attend(prob, pages=None, q=None, **kw):
     return out, lse
 
 
-def check(prob, out, lse, eps=STREAM_EPS):
+def weight_eps(prob):
+    """By the kernel that a call's longest sequence, or a prefix read for the whole batch, goes to."""
+    rows = max(prob.new) * (prob.hq // prob.hkv)
+    return TILE_EPS if rows > 16 or (prob.prefix and len(prob.new) > 1) else STREAM_EPS
+
+
+def check(prob, out, lse):
     ref = prob.reference()
+    eps = weight_eps(prob)
     b_out, b_lse = prob.bounds(ref, eps)
     o, m = out.double().cpu().numpy(), lse.double().cpu().numpy()
     n = sum(prob.new)
@@ -242,6 +251,81 @@ def test_prefix(prefix, new, own, hq, hkv, page, bits):
 def test_sizes_of_values(kw):
     prob = G.Attention(24, [1, 3], [400, 77], 8, 2, 16, 4, **kw)
     check(prob, *attend(prob))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("new,own,hq,hkv,page", [
+    ([129], [129], 1, 1, 16),                       # the second half's first row
+    ([257], [300], 1, 1, 16),                       # the second block's
+    ([200, 130], [200, 500], 8, 2, 64),
+    ([33], [3000], 16, 2, 128),                     # keys of a few rows, split
+    ([1, 64, 2, 5, 0], [50, 64, 900, 5, 77], 8, 2, 32),     # both kernels in one call
+    ([300, 41, 500], [1200, 41, 640], 6, 1, 256),
+    ([9, 20, 70], [4, 10, 60], 4, 1, 16),           # fewer cached tokens than new ones
+    ([100], [100], 128, 2, 16),                     # 64 query heads per KV head
+])
+def test_many_rows(new, own, hq, hkv, page, bits):
+    prob = G.Attention(33, new, own, hq, hkv, page, bits, pad=3)
+    check(prob, *attend(prob))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("rule", [
+    dict(softcap=20.0), dict(window=1), dict(window=130), dict(slopes=True), dict(scale=-0.1), dict(scale=0.0),
+    dict(softcap=30.0, window=300, slopes=True), dict(v_size=1e4), dict(v_size=1e-6), dict(k_size=30.0, q_size=4.0),
+    dict(q_size=1e4, k_size=1e-4)])
+@pytest.mark.parametrize("prefix", [0, 200])
+def test_many_rows_score_rules(rule, prefix, bits):
+    prob = G.Attention(34, [150, 40], [520, 40], 8, 2, 16, bits, prefix=prefix, pad=1, **rule)
+    check(prob, *attend(prob))
+
+
+@pytest.mark.parametrize("rule", [{}, dict(softcap=20.0), dict(window=700), dict(slopes=True)])
+@pytest.mark.parametrize("prefix,batch,new,page,bits", [
+    (1000, 3, 1, 16, 4), (129, 40, 1, 32, 8), (1500, 70, 1, 64, 4), (300, 9, 8, 16, 8), (128, 5, 32, 64, 4)])
+def test_prefix_of_a_batch(prefix, batch, new, page, bits, rule):
+    own = [new + (7 * b) % 90 for b in range(batch)]
+    count = [max(0, new - b % 3) for b in range(batch)]
+    prob = G.Attention(35, count, own, 8, 2, page, bits, prefix=prefix, pad=2, **rule)
+    check(prob, *attend(prob))
+
+
+def test_many_rows_split_and_repeat():
+    prob = G.Attention(36, [40, 3], [2500, 9], 8, 2, 64, 4)
+    a = attend(prob)
+    check(prob, *a)
+    b = attend(prob)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    check(prob, *attend(prob, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda")))
+
+
+def test_waits_that_give_up_are_reported():
+    """Every wait of the tile kernel gives up at once: the call ends, reports, and the next one is right."""
+    prob = G.Attention(37, [40], [400], 8, 2, 64, 4)
+    sq.lib.sq_debug_set_spin_limit(0xFFFFFFFF)
+    try:
+        attend(prob)
+        assert sq.device_status() == 5               # SQ_ERR_TIMEOUT
+    finally:
+        sq.lib.sq_debug_set_spin_limit(0)
+    check(prob, *attend(prob))
+
+
+def test_many_rows_hidden_infinities_do_not_leak():
+    prob = G.Attention(38, [64], [200], 4, 1, 16, 4)
+    ref = prob.reference()
+    pages = pages_of(prob.pool)
+    page, row = prob.table()[0, 199 // 16], 199 % 16
+    for bad, keys in ((float("inf"), "kv"), (float("nan"), "kv"), (float("nan"), "v"), (float("inf"), "v")):
+        for key in "kv":
+            getattr(pages, key + "_scale")[page, :, row] = bad if key in keys else 0.5
+        out, lse = attend(prob, pages)
+        b_out, b_lse = prob.bounds(ref, TILE_EPS)
+        o, m = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        assert (np.abs(o[:63] - ref[0][:63]) <= b_out[:63]).all()
+        assert (np.abs(m[:63] - ref[1][:63]) <= b_lse[:63]).all()
+        if keys == "v":
+            assert not np.isfinite(o[63]).any()
 
 
 def test_long_cache_splits_and_is_repeatable():
