@@ -12,7 +12,7 @@
 //
 // Warps: 0-3 and 4-7 softmax of half 0 and 1 (a thread per row: no exchange
 // between lanes), 8-11 widen codes from global memory into swizzled shared
-// memory, 12 issues the products.  The halves alternate: while one half's
+// memory, 12 issues the products, 13 works out the units.  The halves alternate: while one half's
 // softmax runs, the tensor cores work for the other.
 //
 // Two rows of work: a sequence's own rows over what it sees (splits of a
@@ -21,6 +21,8 @@
 // results (O, m, l) the streaming kernel joins with each sequence's own part.
 #include <cuda_bf16.h>
 #include <math.h>
+
+#include <type_traits>
 
 #include "kv_attend.cuh"
 #include "sq_device.cuh"
@@ -31,17 +33,19 @@ namespace paged {
 
 constexpr int KT = 128;                    // keys per tile
 constexpr int HALF = 128;                  // rows per half
-constexpr int TILE_THREADS = 13 * 32;
+constexpr int TILE_THREADS = 16 * 32;    // warps 14 and 15 fill the last group
+constexpr int UNITS = 3;                   // unit records in flight
 constexpr int PANEL = 128 * 128;           // bytes of 128 rows x 64 fp16
 constexpr int OFF_Q = 0;                   // [half][2 panels]
 constexpr int OFF_K = OFF_Q + 4 * PANEL;   // [stage][2 panels]
 constexpr int OFF_V = OFF_K + 4 * PANEL;
 constexpr int OFF_SK = OFF_V + 4 * PANEL;  // float [4][KT]
 constexpr int OFF_SV = OFF_SK + 4 * KT * 4;
-constexpr int OFF_HID = OFF_SV + 4 * KT * 4;   // uint32 [4][4]: hidden keys
-constexpr int OFF_SVM = OFF_HID + 64;          // float [4][4]: largest value scale of 32 keys
+constexpr int OFF_HID = OFF_SV + 4 * KT * 4;   // uint32 [4][8]: 4 words of hidden keys, 4 of flags
+constexpr int OFF_SVM = OFF_HID + 128;         // float [4][4]: largest value scale of 32 keys
 constexpr int OFF_BARS = OFF_SVM + 64;
-constexpr int TILE_SMEM = OFF_BARS + 256 + 1024;
+constexpr int OFF_UNITS = OFF_BARS + 256;      // TileUnit [UNITS]
+constexpr int TILE_SMEM = OFF_UNITS + UNITS * 128 + 1024;
 constexpr uint32_t TILE_TMEM = 512;        // S0, S1, O0, O1
 constexpr uint32_t IDESC_S = idesc_f16(128, 128, false, false);
 constexpr uint32_t IDESC_O = idesc_f16(128, 128, false, true);
@@ -50,6 +54,7 @@ struct TileBars {
   uint64_t k_full[2], v_full[2], k_free[2], v_free[2], sc_full[4];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
   uint64_t parts, joined, drain;           // partial results written; who joins them is known
+  uint64_t u_full[UNITS], u_free[UNITS];
   uint32_t tmem, last;
 };
 static_assert(sizeof(TileBars) <= 256, "barriers");
@@ -72,7 +77,8 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
       : "memory");
 }
 
-// A unit as every role sees it.
+// A unit as every role sees it.  Warp 13 works them out and hands them on in a ring of records in
+// shared memory: the other roles hold only what they use.  rows 0: no unit follows.
 struct TileUnit {
   int row0;                                // packed row of the first token
   int base, rows;                          // first (token, head) row of the unit, live rows
@@ -85,8 +91,10 @@ struct TileUnit {
   int slot;                                // the unit's place among the units
 };
 
+static_assert(sizeof(TileUnit) <= 128, "unit records");
+
 // Unit `x` of this launch; false if it is empty.
-__device__ __forceinline__ bool tile_unit(const AttnParams& P, int64_t x, TileUnit& u, bool report) {
+__device__ __forceinline__ bool tile_unit(const AttnParams& P, int64_t x, TileUnit& u) {
   const int G = P.G, hkv = P.pages.hkv, R = 2 * HALF;
   u.piece = static_cast<int>(x % P.nsplit);
   const int64_t y = x / P.nsplit;
@@ -128,7 +136,6 @@ __device__ __forceinline__ bool tile_unit(const AttnParams& P, int64_t x, TileUn
   }
   const Seq s = load_seq(P, lo, false);
   const int64_t rows = static_cast<int64_t>(s.qlen) * G;
-  if (report && P.few_rows == 0 && x == 0) load_seq(P, lo, true);
   if (rows <= P.few_rows) return false;    // the streaming kernel's, which reports too
   const int blocks = static_cast<int>((rows + R - 1) / R);
   const int64_t back = place(lo + 1) - 1 - z;
@@ -158,12 +165,18 @@ __device__ __forceinline__ bool tile_unit(const AttnParams& P, int64_t x, TileUn
   return true;
 }
 
+// Position of the first key of tile i of a unit.
+__device__ __forceinline__ int tile_pos(const AttnParams& P, const volatile TileUnit& u, int i) {
+  const int k = u.first + i, pn = u.pn;
+  return k < pn ? (u.pt0 + k) * KT : P.prefix_len + (u.ot0 + k - pn) * KT;
+}
+
 // Tile i of a unit: its first row, row limit and position.
 struct TileAt {
   const int32_t* table;
   int local, limit, kpos;
 };
-__device__ __forceinline__ TileAt tile_at(const AttnParams& P, const TileUnit& u, int i) {
+__device__ __forceinline__ TileAt tile_at(const AttnParams& P, const volatile TileUnit& u, int i) {
   const int k = u.first + i;
   if (k < u.pn) {
     const int l = (u.pt0 + k) * KT;
@@ -185,6 +198,18 @@ __device__ __forceinline__ int64_t unit_index(int k) {
 template <int BITS>
 __device__ __forceinline__ constexpr int place8(int d) {
   return BITS == 8 ? d : (d < 4 ? 2 * d : 2 * (d - 4) + 1);
+}
+
+// Bits 0 .. n - 1, n clamped to 0 .. 32.
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// (a, b) *= (x, y), floats held in registers of tensor-memory transfers.
+__device__ __forceinline__ void mul2u(uint32_t& a, uint32_t& b, float x, float y) {
+  const f2 r = mul2(f2{__uint_as_float(a), __uint_as_float(b)}, f2{x, y});
+  a = __float_as_uint(r.x);
+  b = __float_as_uint(r.y);
 }
 
 // ------------------------------------------------------------ widening
@@ -263,6 +288,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
     mbar_init(&bar.parts, 8);
     mbar_init(&bar.joined, 1);
     mbar_init(&bar.drain, 1);
+    for (int i = 0; i < UNITS; ++i) {
+      mbar_init(&bar.u_full[i], 1);
+      mbar_init(&bar.u_free[i], 13);
+    }
     fence_mbar_init();
   }
   if (warp == 12) {
@@ -273,51 +302,56 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
-  const int64_t units = P.units;
+  TileUnit* ring_u = reinterpret_cast<TileUnit*>(smem + OFF_UNITS);
   bool ok = true;
 
+  // registers, of the 512 x 128 that the block is launched with: 2 x 176 + 88 + 72 (4 bits) or 2 x 168 +
+  // 104 + 72 (8 bits) times 128
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(BITS == 4 ? 176 : 168));
     const int hf = warp >> 2, quarter = warp & 3;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const uint32_t t_s = lane_base + hf * 128, t_o = lane_base + 256 + hf * 128;
     const int r = 32 * quarter + lane;     // row within the half
     int tiles = 0, mine = 0, splits = 0;   // tiles seen by the CTA and by this half; joins
+    const bool special = P.cap > 0.f || P.slopes != nullptr;
     for (int k = 0; ok; ++k) {
-      const int64_t x = unit_index(k);
-      if (k * static_cast<int64_t>(gridDim.x) >= units) break;
-      TileUnit u;
-      if (x >= units || !tile_unit(P, x, u, hf == 0 && tid == 0)) continue;
-      const bool active = hf * HALF < u.rows;
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar.u_full[k % UNITS], (k / UNITS) & 1, spin));
+      if (!ok) break;
+      const volatile TileUnit& u = ring_u[k % UNITS];
+      const int rows = u.rows, n = u.n;
+      if (rows == 0) break;
+      const bool active = hf * HALF < rows;
       const int row = hf * HALF + r;
-      const bool live = row < u.rows;
-      const int rr = min(row, u.rows - 1);
-      const int tok = (u.base + rr) / P.G, head = u.h * P.G + u.base + rr - tok * P.G;
-      int qpos = u.pos0 + tok;
-      if (P.shared) {
-        // the packed token's own sequence
-        int lo = 0, hi = P.batch.B;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (P.batch.cu[mid] <= tok)
-            lo = mid;
-          else
-            hi = mid;
-        }
-        const Seq s = load_seq(P, lo, false);
-        qpos = s.keys ? s.pos0 + tok - s.row0 : -1;
-      }
-      const int64_t out_row = static_cast<int64_t>(u.row0 + tok) * P.hq + head;
-      float f = 1.f, m = -INFINITY, l = 0.f, svr = 0.f, svi = 0.f;
-      const float slope = P.slopes ? P.slopes[head] * kLog2e : 0.f;
+      float f = 1.f, m = -INFINITY, l = 0.f, svr = 0.f, mneg = 0.f;
+      bool far = true;
       if (active) {
+        const int at = u.base + min(row, rows - 1), tok = at / P.G, head = u.h * P.G + at - tok * P.G;
+        int qpos = u.pos0 + tok;
+        if (P.shared) {
+          // the packed token's own sequence
+          int lo = 0, hi = P.batch.B;
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (P.batch.cu[mid] <= tok)
+              lo = mid;
+            else
+              hi = mid;
+          }
+          const Seq s = load_seq(P, lo, false);
+          qpos = s.keys ? s.pos0 + tok - s.row0 : -1;
+        }
+        const float slope = P.slopes ? P.slopes[head] * kLog2e : 0.f;
         // this row's query, scaled by a power of two, in fp16
         const uint4* src = reinterpret_cast<const uint4*>(P.q + (u.row0 + tok) * P.sq + head * D);
+        uint4 qw[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) qw[c] = __ldg(src + c);
         float mx = 0.f;
-#pragma unroll 4
+#pragma unroll
         for (int c = 0; c < 16; ++c) {
-          const uint4 w = __ldg(src + c);
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+          const uint32_t ws[4] = {qw[c].x, qw[c].y, qw[c].z, qw[c].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(ws[e] << 16)),
@@ -332,10 +366,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
         if (f < 0.f) f = -f, qf = -qf;
         if (f == 0.f) f = 1.f, qf = 0.f;
         uint8_t* dst = smem + OFF_Q + hf * 2 * PANEL + r * 128;
-#pragma unroll 4
+#pragma unroll
         for (int c = 0; c < 16; ++c) {
-          const uint4 w = __ldg(src + c);
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+          const uint32_t ws[4] = {qw[c].x, qw[c].y, qw[c].z, qw[c].w};
           float v[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -351,8 +384,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.q_full[hf]);
+        const float ff = special ? 1.0f : f;
 
-        for (int i = 0; i < u.n && ok; ++i, ++mine) {
+        for (int i = 0; i < n && ok; ++i, ++mine) {
           const int ring = (tiles + i) & 3;
           // scores first: they tell that every producer warp has come past the ring's last round, so
           // that a half which skipped units cannot take an older phase of the same parity for this one
@@ -363,147 +397,201 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           tc_fence_after();
           const float4* sk4 = reinterpret_cast<const float4*>(s_sk + ring * KT);
           const float4* sv4 = reinterpret_cast<const float4*>(s_sv + ring * KT);
-          const TileAt at = tile_at(P, u, i);
-          const uint32_t hid[4] = {s_hid[ring * 4], s_hid[ring * 4 + 1], s_hid[ring * 4 + 2],
-                                   s_hid[ring * 4 + 3]};
-          const bool edge = (hid[0] | hid[1] | hid[2] | hid[3]) != 0 || at.kpos + KT - 1 > qpos ||
-                            (P.window > 0 && qpos - at.kpos >= P.window);
-          const bool general = __any_sync(0xffffffffu, edge) || P.cap > 0.f || P.slopes != nullptr;
-          // ---- largest score
-          float mx = -INFINITY;
-          if (!general) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t v[32];
-              tmem_ld32(t_s + 32 * c, v);
+          const int rel = qpos - tile_pos(P, u, i);        // distance to the tile's first key
+          if (special) {
+            // capped or sloped scores, in log2 units, back to tensor memory
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t v[16];
+              tmem_ld16(t_s + 16 * c, v);
               tmem_ld_wait();
+              const float d0 = static_cast<float>(rel - 16 * c);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 s = sk4[8 * c + e];
-                const f2 a = mul2(f2{__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1])},
-                                  f2{s.x, s.y});
-                const f2 b = mul2(f2{__uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3])},
-                                  f2{s.z, s.w});
-                mx = fmaxf(mx, fmaxf(a.x, a.y));
-                mx = fmaxf(mx, fmaxf(b.x, b.y));
-              }
-            }
-            mx *= f;
-          } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t v[32];
-              tmem_ld32(t_s + 32 * c, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                float y = __uint_as_float(v[e]) * s_sk[ring * KT + 32 * c + e] * f;
+              for (int e = 0; e < 16; ++e) {
+                float y = __uint_as_float(v[e]) * s_sk[ring * KT + 16 * c + e] * f;
                 if (P.cap > 0.f) y = P.cap * kLog2e * tanh_score(y);
-                const int dist = qpos - (at.kpos + 32 * c + e);
-                y = fmaf(-slope, static_cast<float>(dist), y);
-                const bool seen = dist >= 0 && (P.window == 0 || dist < P.window) &&
-                                  !((hid[c] >> e) & 1u);
-                y = seen ? y : -INFINITY;
-                mx = fmaxf(mx, y);
-                v[e] = __float_as_uint(y);
+                v[e] = __float_as_uint(fmaf(-slope, d0 - static_cast<float>(e), y));
               }
-              tmem_st32(t_s + 32 * c, v);
+              tmem_st16(t_s + 16 * c, v);
             }
             tmem_st_wait();
           }
-          // ---- references, and the sums rescaled where one has moved far
-          float svmax = 0.f;
+          // keys lo .. hi - 1 of the tile are visible to this row by position
+          const int hi = rel + 1, lo = P.window > 0 ? hi - P.window : 0;
+          const uint32_t flags = s_hid[ring * 8 + 4] | s_hid[ring * 8 + 5] | s_hid[ring * 8 + 6] |
+                                 s_hid[ring * 8 + 7];
+          const bool edge = special || __any_sync(0xffffffffu, hi < KT || lo > 0 || flags != 0u);
+          // 32 scores (times the key's scale; the row's factor follows), hidden ones -inf
+          // (the common case is compiled by itself: branches inside cost it half its rate)
+          auto scores = [&](auto general, uint32_t (&v)[32], int c) {
+            if (!general.value || !special) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) svmax = fmaxf(svmax, s_svm[ring * 4 + w]);
+              for (int e = 0; e < 8; ++e) {
+                const float4 s = sk4[8 * c + e];
+                mul2u(v[4 * e], v[4 * e + 1], s.x, s.y);
+                mul2u(v[4 * e + 2], v[4 * e + 3], s.z, s.w);
+              }
+            }
+            if (general.value) {
+              const uint32_t seen =
+                  bits_below(hi - 32 * c) & ~bits_below(lo - 32 * c) & ~s_hid[ring * 8 + c];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = (seen & (1u << e)) ? v[e] : 0xFF800000u;
+            }
+          };
+          // ---- largest score; the next 32 are on their way while 32 are worked on
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto largest = [&](auto general, uint32_t (&v)[32], int c) {
+            scores(general, v, c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int d = 0; d < 8; d += 2)
+                mx4[e] = fmaxf(mx4[e], fmaxf(__uint_as_float(v[8 * e + d]), __uint_as_float(v[8 * e + d + 1])));
+          };
+          uint32_t va[32], vb[32];
+          tmem_ld32(t_s, va);
+          tmem_ld_wait();
+          if (!edge) {
+#pragma unroll 1
+            for (int c = 0; c < 4; c += 2) {
+              tmem_ld32(t_s + 32 * c + 32, vb);
+              largest(std::false_type(), va, c);
+              tmem_ld_wait();
+              tmem_ld32(t_s + ((32 * c + 64) & 127), va);       // at the end the first again
+              largest(std::false_type(), vb, c + 1);
+              tmem_ld_wait();
+            }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              largest(std::true_type(), va, c);
+              tmem_ld32(t_s + ((32 * c + 32) & 127), va);
+              tmem_ld_wait();
+            }
+          }
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * ff;
+          // ---- references, and the sums rescaled where one has moved far
+          const float4 sm4 = *reinterpret_cast<const float4*>(s_svm + ring * 4);
+          const float svmax = fmaxf(fmaxf(sm4.x, sm4.y), fmaxf(sm4.z, sm4.w));
           const bool raise = mx > m + 15.0f || svmax > svr;
           if (__any_sync(0xffffffffu, raise)) {
             const int e2 = max(1, min(253, static_cast<int>(__float_as_uint(svmax) >> 23) + 1));
             const float nsv = fmaxf(svr, __uint_as_float(static_cast<uint32_t>(e2) << 23));
             const float down = svr > 0.f ? svr / nsv : 0.f;
             svr = nsv;
-            svi = 1.0f / nsv;
             const float nm = fmaxf(m, mx - 14.0f);
             const float fa = m == -INFINITY ? 0.f : ex2(m - nm);
             m = nm;
             l *= fa;
+            // exp2(s - m) / svr is one exponential while both its factors are far from float32's
+            // ends; otherwise 1 / svr is applied by itself
+            far = svr > 1.1529215e18f || svr < 8.6736174e-19f;          // 2^60, 2^-60
+            mneg = m == -INFINITY ? 0.f : -m;
+            if (!far) mneg -= static_cast<float>(static_cast<int>(__float_as_uint(svr) >> 23) - 127);
             if (i > 0) {
               ok = __all_sync(0xffffffffu, mbar_wait(&bar.o_full[hf], (mine - 1) & 1, spin));
               if (!ok) break;
               tc_fence_after();
               const float g = fa * down;
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                uint32_t v[32];
-                tmem_ld32(t_o + 32 * c, v);
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                uint32_t w[16];
+                tmem_ld16(t_o + 16 * c, w);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * g);
-                tmem_st32(t_o + 32 * c, v);
+                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * g);
+                tmem_st16(t_o + 16 * c, w);
               }
               tmem_st_wait();
             }
           }
           // ---- weights
-          const float mneg = m == -INFINITY ? 0.f : -m;
-          const f2 f2f{general ? 1.0f : f, general ? 1.0f : f}, f2m{mneg, mneg}, f2i{svi, svi};
+          const f2 f2f{ff, ff}, f2m{mneg, mneg};
+          const float svi = svr > 0.f ? 1.0f / svr : 0.f;      // used when far
           f2 sum{0.f, 0.f};
+          auto weights = [&](auto general, uint32_t (&v)[32], int c) {
+            scores(general, v, c);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32], o[16];
-            tmem_ld32(t_s + 32 * c, v);
-            tmem_ld_wait();
+            for (int e = 0; e < 16; ++e) {
+              f2 a = fma2(f2{__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])}, f2f, f2m);
+              a = f2{ex2(a.x), ex2(a.y)};
+              sum = add2(sum, a);
+              v[2 * e] = __float_as_uint(a.x);
+              v[2 * e + 1] = __float_as_uint(a.y);
+            }
+            if (general.value && far) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) mul2u(v[2 * e], v[2 * e + 1], svi, svi);
+            }
+            uint32_t some = 0xffffffffu;
+            if (general.value && (flags & 2u)) {      // some value scale is infinite or NaN: not a hidden key's
+              some = 0;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) some |= (__uint_as_float(v[e]) == 0.f ? 0u : 1u) << e;
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              f2 a{__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1])};
-              f2 b{__uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3])};
-              if (!general) {
-                const float4 s = sk4[8 * c + e];
-                a = mul2(a, f2{s.x, s.y});
-                b = mul2(b, f2{s.z, s.w});
-              }
-              a = fma2(a, f2f, f2m);
-              b = fma2(b, f2f, f2m);
-              a = f2{ex2(a.x), ex2(a.y)};
-              b = f2{ex2(b.x), ex2(b.y)};
-              sum = add2(sum, add2(a, b));
               const float4 s = sv4[8 * c + e];
-              f2 wa = mul2(mul2(a, f2i), f2{s.x, s.y}), wb = mul2(mul2(b, f2i), f2{s.z, s.w});
-              if (general) {               // a hidden key's scale may be infinite or NaN
-                wa.x = a.x == 0.f ? 0.f : wa.x;
-                wa.y = a.y == 0.f ? 0.f : wa.y;
-                wb.x = b.x == 0.f ? 0.f : wb.x;
-                wb.y = b.y == 0.f ? 0.f : wb.y;
-              }
-              o[2 * e] = h2_bits(__floats2half2_rn(wa.x, wa.y));
-              o[2 * e + 1] = h2_bits(__floats2half2_rn(wb.x, wb.y));
+              mul2u(v[4 * e], v[4 * e + 1], s.x, s.y);
+              mul2u(v[4 * e + 2], v[4 * e + 3], s.z, s.w);
             }
+            if (general.value && (flags & 2u)) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = (some & (1u << e)) ? v[e] : 0u;
+            }
+            uint32_t o[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              o[e] = h2_bits(__floats2half2_rn(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])));
             tmem_st16(t_s + 16 * c, o);
+          };
+          if (!edge && !far) {
+#pragma unroll 1
+            for (int c = 0; c < 4; c += 2) {
+              tmem_ld32(t_s + 32 * c + 32, vb);
+              tmem_ld_wait();                // before the weights below take the columns' place
+              weights(std::false_type(), va, c);
+              if (c == 0) tmem_ld32(t_s + 64, va);
+              weights(std::false_type(), vb, c + 1);
+              tmem_ld_wait();
+            }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              weights(std::true_type(), va, c);
+              if (c < 3) tmem_ld32(t_s + 32 * c + 32, va);
+              tmem_ld_wait();
+            }
           }
-          l += sum.x + sum.y;
+          l += (sum.x + sum.y) * (far ? 1.0f : svr);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.p_full[hf]);
         }
-        if (ok && u.n > 0) {
+        if (ok && n > 0) {
           ok = __all_sync(0xffffffffu, mbar_wait(&bar.o_full[hf], (mine - 1) & 1, spin));
           tc_fence_after();
         }
       }
-      tiles += u.n;
+      tiles += n;
       if (!ok) break;
       // ---- out
-      const bool split = u.pieces > 1 && !P.shared;
+      const int pieces = u.pieces, slot = u.slot;
+      const bool split = pieces > 1 && !P.shared, live = row < rows;
+      const int at = u.base + min(row, rows - 1), tok = at / P.G, head = u.h * P.G + at - tok * P.G;
+      const int64_t out_row = static_cast<int64_t>(u.row0 + tok) * P.hq + head;
       float* part_o = nullptr;
       if (P.shared) {
-        const int64_t at = static_cast<int64_t>(u.piece) * P.batch.T * P.hq + out_row;
-        part_o = P.ex_o + at * D;
+        const int64_t to = static_cast<int64_t>(u.piece) * P.batch.T * P.hq + out_row;
+        part_o = P.ex_o + to * D;
         if (active && live) {
-          P.ex_ml[2 * at] = m;
-          P.ex_ml[2 * at + 1] = l;
+          P.ex_ml[2 * to] = m;
+          P.ex_ml[2 * to + 1] = l;
         }
       } else if (split) {
-        float* p = P.tpart + (static_cast<int64_t>(u.slot) * P.nsplit + u.piece) * (2 * HALF * (D + 2));
+        float* p = P.tpart + (static_cast<int64_t>(slot) * P.nsplit + u.piece) * (2 * HALF * (D + 2));
         part_o = p + row * D;
         if (active) {
           p[2 * HALF * D + 2 * row] = live ? m : -INFINITY;
@@ -515,7 +603,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
-          if (u.n > 0) {
+          if (n > 0) {
             tmem_ld32(t_o + 32 * c, v);
             tmem_ld_wait();
           }
@@ -525,7 +613,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
 #pragma unroll
             for (int d = 0; d < 8; ++d) {
               const float o = __uint_as_float(v[8 * c8 + place8<BITS>(d)]);
-              y[d] = u.n > 0 && l != 0.f ? o * svr : 0.f;
+              y[d] = n > 0 && l != 0.f ? o * svr : 0.f;
             }
             if (part_o) {
               float4* dst = reinterpret_cast<float4*>(part_o + 32 * c + 8 * c8);
@@ -558,9 +646,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           if (!ok) break;
           if (lane == 0) {
             __threadfence();
-            const unsigned seen = atomicAdd(P.tcount + u.slot, 1u);
-            bar.last = seen == static_cast<unsigned>(u.pieces - 1);
-            if (bar.last) P.tcount[u.slot] = 0;
+            const unsigned seen = atomicAdd(P.tcount + slot, 1u);
+            bar.last = seen == static_cast<unsigned>(pieces - 1);
+            if (bar.last) P.tcount[slot] = 0;
             mbar_arrive(&bar.joined);
           }
         }
@@ -569,11 +657,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
         if (!ok) break;
         if (bar.last) {
           __threadfence();
-          const float* all = P.tpart + static_cast<int64_t>(u.slot) * P.nsplit * (2 * HALF * (D + 2));
-          for (int q = warp; q < u.rows; q += 8) {
+          const float* all = P.tpart + static_cast<int64_t>(slot) * P.nsplit * (2 * HALF * (D + 2));
+          for (int q = warp; q < rows; q += 8) {
             float M = -INFINITY, L = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int p = 0; p < u.pieces; ++p) {
+            for (int p = 0; p < pieces; ++p) {
               const float* pp = all + static_cast<int64_t>(p) * (2 * HALF * (D + 2));
               const float2 ml = __ldcg(reinterpret_cast<const float2*>(pp + 2 * HALF * D) + q);
               const float4 o = __ldcg(reinterpret_cast<const float4*>(pp + q * D) + lane);
@@ -599,9 +687,12 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
         }
         __syncwarp();                      // bar.last has been read: the next unit's write waits for
       }                                    // every warp's next arrival
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.u_free[k % UNITS]);
     }
   } else if (warp < 12) {
     // ----------------------------------------------------------- widening
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(BITS == 4 ? 88 : 104));
     const int pw = warp - 8, t = lane & 3, b3 = lane >> 2;
     // rows of a warp's load instruction; the two rows of a store phase differ in a bit that the
     // lanes' chunks do not use (see widen_rows)
@@ -609,23 +700,24 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
     const int wrow = 32 * pw;
     int tiles = 0;
     for (int k = 0; ok; ++k) {
-      const int64_t x = unit_index(k);
-      if (k * static_cast<int64_t>(gridDim.x) >= units) break;
-      TileUnit u;
-      if (x >= units || !tile_unit(P, x, u, false)) continue;
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar.u_full[k % UNITS], (k / UNITS) & 1, spin));
+      if (!ok) break;
+      const volatile TileUnit& u = ring_u[k % UNITS];
+      if (u.rows == 0) break;
+      const int n = u.n, h = u.h;
       TileCodes<BITS> kc, vc;
       int kz[4], vz[4];
       float sc[4];                         // lane t = 0: key scale; t = 1: value scale
       uint32_t hidden = 0;
       int64_t grp[4];                      // cache rows of the tile being loaded (-1: hidden)
       auto pages = [&](int i, int (&pg)[2]) {
-        const TileAt at = tile_at(P, u, min(i, u.n - 1));
+        const TileAt at = tile_at(P, u, min(i, n - 1));
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int l = at.local + wrow + 16 * j;
           pg[j] = l < at.limit ? at.table[l >> P.pages.lps] : -1;
           if (l < at.limit && (pg[j] < 0 || pg[j] >= P.pages.num_pages)) {
-            if (lane == 0 && u.h == 0) record_status(SQ_ERR_INVALID_ARG);
+            if (lane == 0 && h == 0) record_status(SQ_ERR_INVALID_ARG);
             pg[j] = -1;
           }
         }
@@ -638,7 +730,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           const int l = at.local + wrow + 8 * j + rsub;
           const int page = pg[j >> 1];
           const bool gone = page < 0 || l >= at.limit;
-          grp[j] = gone ? -1 : group_of(P.pages, page, u.h, l & ((1 << P.pages.lps) - 1));
+          grp[j] = gone ? -1 : group_of(P.pages, page, h, l & ((1 << P.pages.lps) - 1));
           hidden |= static_cast<uint32_t>(gone) << (8 * j + rsub);
           sc[j] = 0.f;
           kz[j] = vz[j] = 0;
@@ -667,13 +759,13 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
         }
       };
       int pg[2];
-      if (u.n > 0) {
+      if (n > 0) {
         pages(0, pg);
         load_k(0, pg);
         load_v();
         pages(1, pg);
       }
-      for (int i = 0; i < u.n; ++i, ++tiles) {
+      for (int i = 0; i < n; ++i, ++tiles) {
         const int st = tiles & 1, ring = tiles & 3;
         const uint32_t par = ((tiles >> 1) & 1) ^ 1;   // a fresh barrier counts as free
         ok = __all_sync(0xffffffffu, mbar_wait(&bar.k_free[st], par, spin));
@@ -687,6 +779,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
         if (lane == 0) mbar_arrive(&bar.k_full[st]);
         // scales, hidden keys
         float svm = 0.f;
+        bool bad = false;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int row = wrow + 8 * j + rsub;
@@ -695,48 +788,58 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
             s_sv[ring * KT + row] = sc[j];
             const float a = fabsf(sc[j]);
             svm = fmaxf(svm, a <= 3.0e38f ? a : 0.f);
+            bad |= !(a <= 3.0e38f);
           }
         }
         svm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(svm)));
         const uint32_t hid = __reduce_or_sync(0xffffffffu, hidden);
+        const bool any_bad = __any_sync(0xffffffffu, bad);
         if (lane == 0) {
           s_svm[ring * 4 + pw] = svm;
-          s_hid[ring * 4 + pw] = hid;
+          s_hid[ring * 8 + pw] = hid;
+          s_hid[ring * 8 + 4 + pw] = (hid != 0 ? 1u : 0u) | (any_bad ? 2u : 0u);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.sc_full[ring]);
-        TileCodes<BITS> v_now = vc;
-        if (i + 1 < u.n) {
-          load_k(i + 1, pg);
+        if (i + 1 < n) load_k(i + 1, pg);
+        ok = __all_sync(0xffffffffu, mbar_wait(&bar.v_free[st], par, spin));
+        if (!ok) break;
+        widen_rows<BITS>(smem + OFF_V + st * 2 * PANEL, vc, vz_now, wrow, rsub, t);
+        if (i + 1 < n) {
           load_v();
           pages(i + 2, pg);
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(&bar.v_free[st], par, spin));
-        if (!ok) break;
-        widen_rows<BITS>(smem + OFF_V + st * 2 * PANEL, v_now, vz_now, wrow, rsub, t);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.v_full[st]);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.u_free[k % UNITS]);
     }
   } else {
     // ------------------------------------------------------------ products
-    int tiles = 0, seen[2] = {0, 0}, qs[2] = {0, 0};
-    const uint32_t q_addr = smem_u32(smem + OFF_Q), k_addr = smem_u32(smem + OFF_K),
-                   v_addr = smem_u32(smem + OFF_V);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 12) {
+    int tiles = 0, seen = 0, qs = 0;         // seen, qs: bit h, the parity that half h waits for next
+    const uint64_t q_desc = desc_sw128(smem_u32(smem + OFF_Q)), k_desc = desc_sw128(smem_u32(smem + OFF_K)),
+                   v_desc = desc_sw128_mn(smem_u32(smem + OFF_V), PANEL, 1024);
     for (int k = 0; ok; ++k) {
-      const int64_t x = unit_index(k);
-      if (k * static_cast<int64_t>(gridDim.x) >= units) break;
-      TileUnit u;
-      if (x >= units || !tile_unit(P, x, u, false)) continue;
-      const int halves = u.rows > HALF ? 2 : 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar.u_full[k % UNITS], (k / UNITS) & 1, spin));
+      if (!ok) break;
+      const volatile TileUnit& u = ring_u[k % UNITS];
+      const int rows = u.rows, n = u.n;
+      if (rows == 0) break;
+      const int halves = rows > HALF ? 2 : 1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.u_free[k % UNITS]);
+      // descriptors advance by constants in their low word (addresses / 16): few registers
       auto scores = [&](int h, int tile) {
         if (lane == 0) {
-          const uint32_t a = q_addr + h * 2 * PANEL, b = k_addr + (tile & 1) * 2 * PANEL;
+          const uint64_t a = q_desc + ((h * 2 * PANEL) >> 4), b = k_desc + (((tile & 1) * 2 * PANEL) >> 4);
 #pragma unroll
           for (int s = 0; s < 8; ++s) {
-            const uint32_t off = (s >> 2) * PANEL + (s & 3) * 32;
-            mma_f16_ss(tmem + h * 128, desc_sw128(a + off), desc_sw128(b + off), IDESC_S, s > 0);
+            const uint32_t off = ((s >> 2) * PANEL + (s & 3) * 32) >> 4;
+            mma_f16_ss(tmem + h * 128, a + off, b + off, IDESC_S, s > 0);
           }
           mma_commit(&bar.s_full[h]);
           if (h == halves - 1) mma_commit(&bar.k_free[tile & 1]);
@@ -744,32 +847,36 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
         __syncwarp();
       };
       for (int h = 0; h < halves && ok; ++h) {
-        ok = mbar_wait(&bar.q_full[h], qs[h]++ & 1, spin);
+        ok = mbar_wait(&bar.q_full[h], (qs >> h) & 1, spin);
+        qs ^= 1 << h;
       }
-      if (ok && u.n > 0) ok = mbar_wait(&bar.k_full[tiles & 1], (tiles >> 1) & 1, spin);
+      if (ok && n > 0) ok = mbar_wait(&bar.k_full[tiles & 1], (tiles >> 1) & 1, spin);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      if (u.n > 0)
+      if (n > 0)
+#pragma unroll 1
         for (int h = 0; h < halves; ++h) scores(h, tiles);
-      for (int i = 0; i < u.n && ok; ++i, ++tiles) {
+      for (int i = 0; i < n && ok; ++i, ++tiles) {
+#pragma unroll 1
         for (int h = 0; h < halves && ok; ++h) {
-          ok = mbar_wait(&bar.p_full[h], seen[h]++ & 1, spin);
+          ok = mbar_wait(&bar.p_full[h], (seen >> h) & 1, spin);
+          seen ^= 1 << h;
           if (ok && h == 0) ok = mbar_wait(&bar.v_full[tiles & 1], (tiles >> 1) & 1, spin);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           if (lane == 0) {
-            const uint32_t b = v_addr + (tiles & 1) * 2 * PANEL;
+            const uint64_t b = v_desc + (((tiles & 1) * 2 * PANEL) >> 4);
 #pragma unroll
             for (int s = 0; s < 8; ++s)
-              mma_f16_ts(tmem + 256 + h * 128, tmem + h * 128 + 8 * s,
-                         desc_sw128_mn(b + s * 2048, PANEL, 1024), IDESC_O, i > 0 || s > 0);
+              mma_f16_ts(tmem + 256 + h * 128, tmem + h * 128 + 8 * s, b + s * (2048 >> 4), IDESC_O,
+                         i > 0 || s > 0);
             mma_commit(&bar.o_full[h]);
             if (h == halves - 1) mma_commit(&bar.v_free[tiles & 1]);
           }
           __syncwarp();
-          if (i + 1 < u.n) {
+          if (i + 1 < n) {
             if (h == 0) {
               ok = __all_sync(0xffffffffu,
                               mbar_wait(&bar.k_full[(tiles + 1) & 1], ((tiles + 1) >> 1) & 1, spin));
@@ -787,6 +894,29 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
       mbar_wait(&bar.drain, 0, 0);
     }
     __syncwarp();
+    } else if (warp == 13) {
+      // ------------------------------------------------------------- units
+      const int64_t units = P.units;
+      int at = 0;
+      bool more = true;
+      // no streaming kernel follows a call of one long sequence: its lengths are checked here
+      if (P.few_rows == 0 && !P.shared && blockIdx.x == 0 && lane == 0) load_seq(P, 0, true);
+      for (int k = 0; ok && more; ++k) {
+        more = k * static_cast<int64_t>(gridDim.x) < units;
+        const int64_t x = unit_index(k);
+        TileUnit u;
+        u.rows = 0;
+        if (more && (x >= units || !tile_unit(P, x, u))) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bar.u_free[at % UNITS], ((at / UNITS) & 1) ^ 1, spin));
+        if (!ok) break;
+        if (lane == 0) {
+          ring_u[at % UNITS] = u;
+          mbar_arrive(&bar.u_full[at % UNITS]);
+        }
+        __syncwarp();
+        ++at;
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
