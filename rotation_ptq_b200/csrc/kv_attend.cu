@@ -2,22 +2,37 @@
 // sm_100a: the streaming kernel.
 //
 // With rows = (new tokens) x (query heads per KV head) of one KV head, this
-// kernel computes, over tiles of 64 keys,
-//     S^T = K_int Q^T,   s = S sk f_row,   w = exp2(s - m) sv,   O^T += V_int^T w
-// where K_int, V_int are codes less zero points (integers in [-255, 255],
-// exact in fp16), sk and sv the row scales, applied in float32.  Its time is
-// that of streaming the cache: 4 x 16-row-code products per loaded byte are
-// far below the tensor pipe, so the products are warp-level m16n8k16 MMAs
-// whose operands come straight from the loaded words without a trip through
-// shared memory (a tcgen05 operand would have to be widened into swizzled
-// shared memory and synchronised per tile: more work than the product).
+// kernel computes, over tiles of 64 keys (16 per warp),
+//     S^T = C_k Q^T,   s = (S - z_k sum q) sk f_row,   w = exp2(s - m) sv,
+//     O^T += (C_v - z_v)^T w
+// with C the codes as they are stored, z the zero points and sk, sv the row
+// scales, applied in float32.  The products are warp-level m16n8k16 MMAs whose
+// operands come straight from the loaded words (a tcgen05 operand would have
+// to be widened into swizzled shared memory and synchronised per tile: more
+// work than the product).  A code n is used as the fp16 bit pattern n, the
+// subnormal n 2^-24: one mask widens two codes; a mask that leaves a nibble
+// four bits higher gives 16 n 2^-24, which the query's element (or the
+// output's channel) takes back by an exact power of two.  The keys' zero
+// points come back once per key and row: 128 terms' sums differ by 2^-24 of
+// themselves.  The values' are subtracted before the product (exactly): a sum
+// over a long cache of codes that are all positive would lose, against one of
+// both signs, what its mean is larger than the result.
+//
+// What bounds it: issue slots, then the cache's bytes.  A warp's step of 16
+// keys x 128 channels took 592 instructions with codes widened to whole
+// numbers and loads straight to registers (long 4-bit caches: 158 us for 280
+// MB); see the end of this file for what it takes now.  Loads go through a
+// ring of 16-key slots in shared memory per warp (cp.async, no exchange
+// between warps), D - 1 slots ahead.
 //
 // Exactness: queries are scaled per row by a power of two that puts the
 // largest at 2^14..2^15 and held in fp16 (a bf16 value has 8 significant
-// bits, so only values 2^-29 and more below the row's largest lose any);
+// bits, so only values 2^-25 and more below the row's largest lose any);
 // products are exact and summed in float32.  Weights are held as the sum of
 // two fp16 numbers (22 bits, down to 2^-38 of a row's largest) so that their
-// rounding stays below float32 sums'.
+// rounding stays below float32 sums'.  With up to 4 rows (PAIR) the product's
+// columns 4..7 repeat rows 0..3 and carry the weights' low parts, so that both
+// parts take one MMA.
 //
 // Fragment layout (lane = 4 g + t): the MMA's k order is free as long as both
 // operands agree, so lane (g, t) takes row g's t-th contiguous run of codes
@@ -30,6 +45,8 @@
 // them in the order of the list, so results do not depend on arrival order.
 #include <cuda_bf16.h>
 #include <math.h>
+
+#include <atomic>
 
 #include "kv_attend.cuh"
 #include "kv_quant.cuh"
@@ -61,14 +78,18 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
-template <int BITS>
-struct KFrag {                             // a lane's codes of one key row: 32
-  uint4 c[BITS / 4];
-};
-template <int BITS>
-struct VFrag {                             // 16 dims of one key row
-  uint2 c[BITS / 4];
-};
+__device__ __forceinline__ uint32_t add_bits(uint32_t a, uint32_t b) {
+  return h2_bits(__hadd2(bits_h2(a), bits_h2(b)));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // A unit: one sequence, block of rows and KV head.
 struct Unit {
@@ -76,19 +97,35 @@ struct Unit {
   int b, h, row0, rows;                    // row0: first of its (token, head) rows
 };
 
-template <int BITS, int NT>
+template <int BITS, int NT, bool PAIR>
 struct Stream {
-  static constexpr int R = 8 * NT;         // rows per unit
+  static constexpr int R = PAIR ? 4 : 8 * NT;            // rows per unit
   static constexpr int RB = D * BITS / 8;
-  static constexpr int KW = 2 * BITS;      // words of a lane's K run
+  static constexpr int DEPTH = BITS == 4 ? 4 : 3;        // ring slots per warp
+  // a slot: 16 keys' K codes, V codes, K scales, V scales, K zero points, V zero points
+  static constexpr int V0 = 16 * RB, SC0 = 32 * RB, SLOT = 32 * RB + 160;
+  static constexpr int RING = DEPTH * SLOT;
+  static constexpr int SMEM = WARPS * (RING + R * D * 4);
+  static constexpr int CTAS = NT == 1 ? (BITS == 4 ? 4 : 3) : 3;
+
+  // Where 16-byte chunk c of key row r lies: rows are permuted inside 128-byte lines so that the
+  // lanes of a load phase, two keys apart (V) or one (K), do not share banks.
+  static __device__ __forceinline__ int k_at(int r, int c) {
+    return BITS == 4 ? r * 64 + c * 16 : r * 128 + ((c ^ ((r & 1) << 2)) << 4);
+  }
+  static __device__ __forceinline__ int v_at(int r, int c) {
+    return BITS == 4 ? (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ (((r >> 1) & 3) << 1)) << 4)
+                     : r * 128 + ((c ^ (((r >> 1) & 3) << 1)) << 4);
+  }
 
   // Query fragments of the unit's rows, and each of this thread's two columns'
   // factor (log2 units, or plain when the scores are capped).
   static __device__ __forceinline__ void load_q(const AttnParams& P, const Unit& u, int g, int t,
-                                                uint32_t (&qb)[NT][8][2], float (&qf)[NT][2]) {
+                                                uint32_t (&qb)[NT][8][2], float (&qf)[NT][2],
+                                                float (&qs)[NT][2]) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int r = 8 * n + g;
+      const int r = PAIR ? g & 3 : 8 * n + g;
       float x[32];
       const bool live = r < u.rows;
       const int row = u.row0 + (live ? r : 0);
@@ -116,30 +153,41 @@ struct Stream {
       const int up = mx > 0.f ? max(-126, min(126, 14 - ex)) : 0;
       const float f = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
       const float inv = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+      // 4-bit codes of the second register of a pair are 16 n 2^-24
+      const float fb = BITS == 4 ? f * 0.0625f : f;
+      float sum = 0.f;
 #pragma unroll
       for (int st = 0; st < 8; ++st) {
-        // the pairs that widen_nibbles / widen_bytes leave
+        // the pairs that the masks below leave
         const float* y = x + (BITS == 4 ? 8 * (st >> 1) : 4 * st);
         const int i0 = BITS == 4 ? 2 * (st & 1) : 0;
         const int a0 = i0, a1 = BITS == 4 ? i0 + 4 : 1, b0 = BITS == 4 ? i0 + 1 : 2,
                   b1 = BITS == 4 ? i0 + 5 : 3;
         qb[n][st][0] = live ? h2_bits(__floats2half2_rn(y[a0] * f, y[a1] * f)) : 0u;
-        qb[n][st][1] = live ? h2_bits(__floats2half2_rn(y[b0] * f, y[b1] * f)) : 0u;
+        qb[n][st][1] = live ? h2_bits(__floats2half2_rn(y[b0] * fb, y[b1] * fb)) : 0u;
+        const float2 lo = __half22float2(bits_h2(qb[n][st][0])), hi = __half22float2(bits_h2(qb[n][st][1]));
+        sum += (lo.x + lo.y) + (hi.x + hi.y) * (BITS == 4 ? 16.0f : 1.0f);
       }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      sum *= 5.9604645e-08f;               // codes are n 2^-24
       // the factor of row 8 n + g lives in its lanes; columns 2t, 2t + 1 need rows 2t, 2t + 1
-      const float mine = inv * P.scale * (P.cap > 0.f ? 1.0f / P.cap : kLog2e);
+      const float mine = inv * 16777216.0f * P.scale * (P.cap > 0.f ? 1.0f / P.cap : kLog2e);
+      qs[n][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
+      qs[n][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
       qf[n][0] = __shfl_sync(0xffffffffu, mine, 8 * t);
       qf[n][1] = __shfl_sync(0xffffffffu, mine, 8 * t + 4);
     }
   }
 };
 
-template <int BITS, int NT>
-__global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 3) stream_kernel(const AttnParams P) {
-  using St = Stream<BITS, NT>;
-  constexpr int R = St::R, RB = St::RB;
-  __shared__ float sm_o[WARPS][R][D];
-  __shared__ float sm_m[WARPS][R], sm_l[WARPS][R];
+template <int BITS, int NT, bool PAIR>
+__global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_kernel(const AttnParams P) {
+  using St = Stream<BITS, NT, PAIR>;
+  constexpr int R = St::R, RB = St::RB, DEPTH = St::DEPTH;
+  extern __shared__ __align__(128) uint8_t stream_smem[];
+  float(*sm_o)[R][D] = reinterpret_cast<float(*)[R][D]>(stream_smem + WARPS * St::RING);
+  __shared__ float sm_m[WARPS][R], sm_l[WARPS][R], sm_f[THREADS], sm_fl[THREADS], sm_top[R];
   __shared__ int64_t sm_scan[WARPS];
   __shared__ int64_t sm_total, sm_base;
   __shared__ int sm_b;
@@ -175,10 +223,10 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 3) stream_kernel(const 
     total += sm_scan[w];
   }
   const int64_t excl = before + incl - mine;
-  // every CTA of the list holds a tile, so a unit's pieces belong to consecutive CTAs
-  const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const int64_t r0 = total * blockIdx.x / ctas, r1 = total * (blockIdx.x + 1) / ctas;
+  // equal pieces but for the last; a unit's pieces belong to consecutive CTAs
+  const int64_t piece = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t r0 = piece * blockIdx.x, r1 = min(total, r0 + piece);
+  if (r0 >= r1) return;
   if (r0 >= excl && r0 < excl + mine) {
     int b = tid * chunk;
     int64_t base = excl;
@@ -217,9 +265,71 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 3) stream_kernel(const 
     cur += i1 - i0;
     const int first = split ? i0 : 0, last = split ? min(i1, u.s.tiles()) : u.s.tiles();
 
+    // ---- where the warp's keys of tile i are, and their way into the ring
+    const uint8_t* ring = stream_smem + warp * St::RING;
+    const uint32_t ring32 = smem_u32(ring);
+    struct Keys {
+      int local, limit, kpos;              // first row of 16, rows of its pages, position of the first
+      const int32_t* table;
+    };
+    auto keys_of = [&](int i) {
+      const bool pre = i < u.s.pn;
+      Keys k;
+      k.local = (pre ? u.s.pt0 + i : u.s.ot0 + i - u.s.pn) * TILE + 16 * warp;
+      k.limit = pre ? P.prefix_len : u.s.len;
+      k.kpos = (pre ? 0 : P.prefix_len) + k.local;
+      k.table = pre ? P.prefix_table : P.batch.table + static_cast<int64_t>(u.b) * P.batch.width;
+      return k;
+    };
+    auto page_of = [&](int i) {            // -1: no keys
+      if (i >= last) return -1;
+      const Keys k = keys_of(i);
+      return k.local < k.limit ? k.table[k.local >> P.pages.lps] : -1;
+    };
+    unsigned filled = 0;                   // bit slot: it holds keys
+    // lanes 0..3 fetch the K scales, 4..7 the V scales, 8 and 9 the zero points
+    const uint8_t* extra = reinterpret_cast<const uint8_t*>(lane < 4 ? P.pages.ks : P.pages.vs) + 16 * (lane & 3);
+    if (lane == 8) extra = P.pages.kz;
+    if (lane == 9) extra = P.pages.vz;
+    const int extra_step = lane < 8 ? 4 : 1;
+    auto fetch = [&](int i, int page, int slot) {
+      filled &= ~(1u << slot);
+      if (i < last) {
+        const Keys k = keys_of(i);
+        if (k.local < k.limit) {
+          if (page < 0 || page >= P.pages.num_pages) {
+            if (lane == 0) record_status(SQ_ERR_INVALID_ARG);
+          } else {
+            const int64_t grp = group_of(P.pages, page, u.h, k.local & ((1 << P.pages.lps) - 1));
+            const uint32_t dst = ring32 + slot * St::SLOT;
+            const uint8_t* kc = P.pages.kc + grp * RB + 16 * lane;
+            const uint8_t* vc = P.pages.vc + grp * RB + 16 * lane;
+            constexpr int CPR = RB / 16, RPI = 32 / CPR;         // chunks per row, rows per instruction
+#pragma unroll
+            for (int j = 0; j < 16 / RPI; ++j) {
+              const int r = j * RPI + lane / CPR, c = lane % CPR;
+              cp_async16(dst + St::k_at(r, c), kc + 512 * j);
+              cp_async16(dst + St::V0 + St::v_at(r, c), vc + 512 * j);
+            }
+            if (lane < 10) cp_async16(dst + St::SC0 + 16 * lane, extra + grp * extra_step);
+            filled |= 1u << slot;
+          }
+        }
+      }
+      cp_async_commit();
+    };
+    {
+      int pages[DEPTH];
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) pages[d] = page_of(first + d);
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) fetch(first + d, pages[d], d);
+    }
+    int page_next = page_of(first + DEPTH);
+
     uint32_t qb[NT][8][2];
-    float qf[NT][2];
-    St::load_q(P, u, g, t, qb, qf);
+    float qf[NT][2], qs[NT][2];
+    St::load_q(P, u, g, t, qb, qf, qs);
     // this thread's columns: rows 8 n + 2 t + {0, 1}
     int qpos[NT][2];
     float slope[NT][2];
@@ -227,11 +337,12 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 3) stream_kernel(const 
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = min(8 * n + 2 * t + e, u.rows - 1);
+        const int r = min(PAIR ? 2 * (t & 1) + e : 8 * n + 2 * t + e, u.rows - 1);
         const int tok = (u.row0 + r) / G;
         qpos[n][e] = u.s.pos0 + tok;
         slope[n][e] = P.slopes ? P.slopes[u.h * G + u.row0 + r - tok * G] * kLog2e : 0.f;
       }
+    const int qmin = u.s.pos0 + u.row0 / G, qmax = u.s.pos0 + (u.row0 + u.rows - 1) / G;
 
     float o[NT][8][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -245,222 +356,240 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 3) stream_kernel(const 
     }
     float svr = 0.f, svi = 0.f;            // power of two at or above the value scales so far; 1 / svr
 
-    for (int i = first; i < last; ++i) {
-      const bool pre = i < u.s.pn;
-      const int local = (pre ? u.s.pt0 + i : u.s.ot0 + i - u.s.pn) * TILE + 16 * warp;
-      const int limit = pre ? P.prefix_len : u.s.len;
-      if (local >= limit) continue;
-      const int kpos0 = (pre ? 0 : P.prefix_len) + local;      // position of the warp's first key
-      const int32_t* table =
-          pre ? P.prefix_table : P.batch.table + static_cast<int64_t>(u.b) * P.batch.width;
-      const int page = table[local >> P.pages.lps];
-      if (page < 0 || page >= P.pages.num_pages) {
-        if (lane == 0) record_status(SQ_ERR_INVALID_ARG);
-        continue;
-      }
-      const int64_t grp = group_of(P.pages, page, u.h, local & ((1 << P.pages.lps) - 1));
-      // ---- loads
-      KFrag<BITS> kf[2];
-      VFrag<BITS> vf[4];
+    int slot = 0;
+    for (int i = first; i < last; ++i, slot = slot + 1 == DEPTH ? 0 : slot + 1) {
+      cp_async_wait<DEPTH - 1>();
+      __syncwarp();
+      if ((filled >> slot) & 1u) {
+        const uint8_t* sl = ring + slot * St::SLOT;
+        const Keys k = keys_of(i);
+        float sk[2], sv[2], kz[2];
+        uint32_t vz[2];                    // less the zero points of keys 2t, 2t + 1 (+ 8): fp16 -z 2^-24
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const uint4* src = reinterpret_cast<const uint4*>(P.pages.kc + (grp + g + 8 * hf) * RB) + t;
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint8_t* x = sl + St::SC0;
+          sk[hf] = reinterpret_cast<const float*>(x)[g + 8 * hf];
+          sv[hf] = reinterpret_cast<const float*>(x)[16 + g + 8 * hf];
+          kz[hf] = static_cast<float>(x[128 + g + 8 * hf]);
+          const uint32_t zz = reinterpret_cast<const uint16_t*>(x + 144)[t + 4 * hf];
+          vz[hf] = __byte_perm(zz, 0u, 0x4140u) | 0x80008000u;
+        }
+        // ---- S^T = C_k Q^T
+        float sc[NT][4];
 #pragma unroll
-        for (int c = 0; c < BITS / 4; ++c) kf[hf].c[c] = __ldg(src + 4 * c);
-      }
+        for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int key = 2 * t + (j & 1) + 8 * (j >> 1);
-        const uint2* src =
-            reinterpret_cast<const uint2*>(P.pages.vc + (grp + key) * RB + g * (RB / 8));
+        for (int c = 0; c < BITS / 4; ++c) {
+          const uint4 a4 = *reinterpret_cast<const uint4*>(sl + St::k_at(g, t + 4 * c));
+          const uint4 b4 = *reinterpret_cast<const uint4*>(sl + St::k_at(g + 8, t + 4 * c));
+          const uint32_t wa[4] = {a4.x, a4.y, a4.z, a4.w}, wb[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
-        for (int c = 0; c < BITS / 4; ++c) vf[j].c[c] = __ldg(src + c);
-      }
-      float sk[2], sv[2];
-      __half2 kz1[2], kz16[2], vz1[2], vz16[2];
+          for (int w = 0; w < 4; ++w) {
+            if (BITS == 4) {
+              const uint32_t a8 = wa[w] >> 8, b8 = wb[w] >> 8;
+              const uint32_t f0[4] = {wa[w] & 0x000F000Fu, wb[w] & 0x000F000Fu, wa[w] & 0x00F000F0u,
+                                      wb[w] & 0x00F000F0u};
+              const uint32_t f1[4] = {a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u,
+                                      b8 & 0x00F000F0u};
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        sk[hf] = __ldg(P.pages.ks + grp + g + 8 * hf);
-        sv[hf] = __ldg(P.pages.vs + grp + g + 8 * hf);
-        const int z = __ldg(P.pages.kz + grp + g + 8 * hf);
-        kz1[hf] = __half2half2(__int2half_rn(-1024 - z));
-        kz16[hf] = __half2half2(__int2half_rn(-64 - z));
-        const uint32_t zz =
-            __ldg(reinterpret_cast<const uint16_t*>(P.pages.vz + grp) + t + 4 * hf);
-        const int za = zz & 0xFF, zb = zz >> 8;
-        vz1[hf] = __halves2half2(__int2half_rn(-1024 - za), __int2half_rn(-1024 - zb));
-        vz16[hf] = __halves2half2(__int2half_rn(-64 - za), __int2half_rn(-64 - zb));
-      }
-      // ---- S^T = K_int Q^T
-      float sc[NT][4];
+              for (int n = 0; n < NT; ++n) {
+                mma16816(sc[n], f0, qb[n][2 * w][0], qb[n][2 * w][1]);
+                mma16816(sc[n], f1, qb[n][2 * w + 1][0], qb[n][2 * w + 1][1]);
+              }
+            } else {
+              const uint32_t f0[4] = {__byte_perm(wa[w], 0u, 0x4140u), __byte_perm(wb[w], 0u, 0x4140u),
+                                      __byte_perm(wa[w], 0u, 0x4342u), __byte_perm(wb[w], 0u, 0x4342u)};
 #pragma unroll
-      for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
-      const uint32_t* w0 = reinterpret_cast<const uint32_t*>(kf[0].c);
-      const uint32_t* w1 = reinterpret_cast<const uint32_t*>(kf[1].c);
-#pragma unroll
-      for (int w = 0; w < BITS; ++w) {
-        if (BITS == 4) {
-          uint32_t x[4], y[4];
-          widen_nibbles(w0[w], kz1[0], kz16[0], x);
-          widen_nibbles(w1[w], kz1[1], kz16[1], y);
-          const uint32_t a0[4] = {x[0], y[0], x[1], y[1]}, a1[4] = {x[2], y[2], x[3], y[3]};
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma16816(sc[n], a0, qb[n][2 * w][0], qb[n][2 * w][1]);
-            mma16816(sc[n], a1, qb[n][2 * w + 1][0], qb[n][2 * w + 1][1]);
+              for (int n = 0; n < NT; ++n) mma16816(sc[n], f0, qb[n][4 * c + w][0], qb[n][4 * c + w][1]);
+            }
           }
-        } else {
-          uint32_t x[2], y[2];
-          widen_bytes(w0[w], kz1[0], x);
-          widen_bytes(w1[w], kz1[1], y);
-          const uint32_t a[4] = {x[0], y[0], x[1], y[1]};
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816(sc[n], a, qb[n][w][0], qb[n][w][1]);
         }
-      }
-      // ---- scores: [n][0], [1] key g; [2], [3] key g + 8; columns 2t, 2t + 1
-      bool raise = false;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int hf = e >> 1, c = e & 1;
-          float x = sc[n][e] * sk[hf] * qf[n][c];
-          if (P.cap > 0.f) x = P.cap * kLog2e * tanh_score(x);
-          const int dist = qpos[n][c] - (kpos0 + g + 8 * hf);
-          x = fmaf(-slope[n][c], static_cast<float>(dist), x);
-          const bool seen =
-              dist >= 0 && (P.window == 0 || dist < P.window) && local + g + 8 * hf < limit;
-          sc[n][e] = seen ? x : -INFINITY;
-          raise |= sc[n][e] > m[n][c] + (kLift + kLazy);
-        }
-      // ---- references: rescale only when a maximum has moved far
-      float svmax = 0.f;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {     // infinities and NaN, and rows behind the last key, set none
-        const float a = fabsf(sv[hf]);
-        svmax = fmaxf(svmax, local + g + 8 * hf < limit && a <= 3.0e38f ? a : 0.f);
-      }
-      raise |= svmax > svr;
-      if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-        for (int of = 4; of < 32; of <<= 1)
-          svmax = fmaxf(svmax, __shfl_xor_sync(0xffffffffu, svmax, of));
-        // a power of two at or above svmax, between 2^-126 and 2^126
-        const int e2 = max(1, min(253, static_cast<int>(__float_as_uint(svmax) >> 23) + 1));
-        const float nsv = fmaxf(svr, __uint_as_float(static_cast<uint32_t>(e2) << 23));
-        const float down = svr > 0.f ? svr / nsv : 0.f;
-        svr = nsv;
-        svi = 1.0f / nsv;
+        // ---- scores: [n][0], [1] key g; [2], [3] key g + 8; columns 2t, 2t + 1
+        const bool plain = P.cap <= 0.f && P.slopes == nullptr && k.local + 16 <= k.limit &&
+                           k.kpos + 15 <= qmin && (P.window == 0 || qmax - k.kpos < P.window);
+        bool raise = false;
+        float svmax = 0.f;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float mx = fmaxf(fmaxf(sc[n][c], sc[n][2 + c]) - kLift, m[n][c]);
+          for (int e = 0; e < 4; ++e)
+            sc[n][e] = fmaf(-kz[e >> 1], qs[n][e & 1], sc[n][e]) * (sk[e >> 1] * qf[n][e & 1]);
+        if (!plain) {
 #pragma unroll
-            for (int of = 4; of < 32; of <<= 1)
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, of));
-            const float f = m[n][c] == -INFINITY ? 0.f : ex2(m[n][c] - mx);
-            m[n][c] = mx;
-            l[n][c] *= f;
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i8 = 0; i8 < 8; ++i8) {
-              o[n][i8][c] *= f * down;
-              o[n][i8][2 + c] *= f * down;
+            for (int e = 0; e < 4; ++e) {
+              const int hf = e >> 1, c = e & 1;
+              float x = sc[n][e];
+              if (P.cap > 0.f) x = P.cap * kLog2e * tanh_score(x);
+              const int dist = qpos[n][c] - (k.kpos + g + 8 * hf);
+              x = fmaf(-slope[n][c], static_cast<float>(dist), x);
+              const bool seen =
+                  dist >= 0 && (P.window == 0 || dist < P.window) && k.local + g + 8 * hf < k.limit;
+              sc[n][e] = seen ? x : -INFINITY;
+            }
+          // rows behind the last key hold anything
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+            if (k.local + g + 8 * hf >= k.limit) sv[hf] = 0.f;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) raise |= sc[n][e] > m[n][e & 1] + (kLift + kLazy);
+        // ---- references: rescale only when a maximum has moved far
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {   // infinities and NaN set none
+          const float a = fabsf(sv[hf]);
+          svmax = fmaxf(svmax, a <= 3.0e38f ? a : 0.f);
+        }
+        raise |= svmax > svr;
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int of = 4; of < 32; of <<= 1)
+            svmax = fmaxf(svmax, __shfl_xor_sync(0xffffffffu, svmax, of));
+          // a power of two at or above svmax, between 2^-126 and 2^126
+          const int e2 = max(1, min(253, static_cast<int>(__float_as_uint(svmax) >> 23) + 1));
+          const float nsv = fmaxf(svr, __uint_as_float(static_cast<uint32_t>(e2) << 23));
+          const float down = svr > 0.f ? svr / nsv : 0.f;
+          svr = nsv;
+          svi = 1.0f / nsv;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float mx = fmaxf(fmaxf(sc[n][c], sc[n][2 + c]) - kLift, m[n][c]);
+#pragma unroll
+              for (int of = 4; of < 32; of <<= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, of));
+              const float f = m[n][c] == -INFINITY ? 0.f : ex2(m[n][c] - mx);
+              m[n][c] = mx;
+              l[n][c] *= f;
+#pragma unroll
+              for (int i8 = 0; i8 < 8; ++i8) {
+                o[n][i8][c] *= f * down;
+                o[n][i8][2 + c] *= f * down;
+              }
+            }
+        }
+        // ---- weights, as fp16 pairs (high, low), to the B operand's layout
+        uint32_t ph[NT][2], pl[NT][2];
+        const float wv[2] = {sv[0] * svi, sv[1] * svi};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float p[4], w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[e] = ex2(sc[n][e] - m[n][e & 1]);
+            w[e] = p[e] * wv[e >> 1];
+          }
+          if (!plain) {                    // no reference yet, or a hidden key's infinite scale
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (sc[n][e] == -INFINITY) p[e] = 0.f;
+              if (p[e] == 0.f) w[e] = 0.f;
             }
           }
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const float w0 = w[2 * hf], w1 = w[2 * hf + 1];
+            l[n][0] += p[2 * hf];
+            l[n][1] += p[2 * hf + 1];
+            const __half2 hi = __floats2half2_rn(w0, w1);
+            const float2 back = __half22float2(hi);
+            const uint32_t lo = h2_bits(__floats2half2_rn(w0 - back.x, w1 - back.y));
+            if (PAIR) {
+              ph[n][hf] = transpose8x8(t < 2 ? h2_bits(hi) : lo);
+            } else {
+              ph[n][hf] = transpose8x8(h2_bits(hi));
+              pl[n][hf] = transpose8x8(lo);
+            }
+          }
+        }
+        // ---- O^T += C_v^T w: dims 16 g + 2 i + {0, 1} in m-tile i
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t va[8], vb[8];           // 8 dims of key pairs (2t, 2t+1) and (2t+8, 2t+9)
+#pragma unroll
+          for (int pr = 0; pr < 2; ++pr) {
+            uint32_t(&dst)[8] = pr ? vb : va;
+            if (BITS == 4) {
+              const int at = 8 * (g & 1) + 4 * half;
+              const uint32_t vz16 = ((vz[pr] & 0x000F000Fu) << 4) | 0x80008000u;
+              const uint32_t a = *reinterpret_cast<const uint32_t*>(
+                  sl + St::V0 + St::v_at(2 * t + 8 * pr, g >> 1) + at);
+              const uint32_t bb = *reinterpret_cast<const uint32_t*>(
+                  sl + St::V0 + St::v_at(2 * t + 1 + 8 * pr, g >> 1) + at);
+#pragma unroll
+              for (int hw = 0; hw < 2; ++hw) {
+                const uint32_t mix = __byte_perm(a, bb, hw ? 0x7632u : 0x5410u), m8 = mix >> 8;
+                dst[4 * hw] = add_bits(mix & 0x000F000Fu, vz[pr]);
+                dst[4 * hw + 1] = add_bits(mix & 0x00F000F0u, vz16);
+                dst[4 * hw + 2] = add_bits(m8 & 0x000F000Fu, vz[pr]);
+                dst[4 * hw + 3] = add_bits(m8 & 0x00F000F0u, vz16);
+              }
+            } else {
+              const uint2 a2 = *reinterpret_cast<const uint2*>(
+                  sl + St::V0 + St::v_at(2 * t + 8 * pr, g) + 8 * half);
+              const uint2 b2 = *reinterpret_cast<const uint2*>(
+                  sl + St::V0 + St::v_at(2 * t + 1 + 8 * pr, g) + 8 * half);
+#pragma unroll
+              for (int hw = 0; hw < 2; ++hw) {
+                const uint32_t a = hw ? a2.y : a2.x, bb = hw ? b2.y : b2.x;
+                const uint32_t lo = __byte_perm(a, bb, 0x5140u), hi = __byte_perm(a, bb, 0x7362u);
+                dst[4 * hw] = add_bits(__byte_perm(lo, 0u, 0x4140u), vz[pr]);
+                dst[4 * hw + 1] = add_bits(__byte_perm(lo, 0u, 0x4342u), vz[pr]);
+                dst[4 * hw + 2] = add_bits(__byte_perm(hi, 0u, 0x4140u), vz[pr]);
+                dst[4 * hw + 3] = add_bits(__byte_perm(hi, 0u, 0x4342u), vz[pr]);
+              }
+            }
+          }
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) {
+            const uint32_t a[4] = {va[2 * i4], va[2 * i4 + 1], vb[2 * i4], vb[2 * i4 + 1]};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma16816(o[n][4 * half + i4], a, ph[n][0], ph[n][1]);
+              if (!PAIR) mma16816(o[n][4 * half + i4], a, pl[n][0], pl[n][1]);
+            }
+          }
+        }
+        __syncwarp();
       }
-      // ---- weights, as fp16 pairs (high, low), to the B operand's layout
-      uint32_t ph[NT][2], pl[NT][2];
-      const float wv[2] = {sv[0] * svi, sv[1] * svi};
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float w[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float x = sc[n][2 * hf + c];
-            const float p = x == -INFINITY ? 0.f : ex2(x - m[n][c]);
-            l[n][c] += p;
-            w[c] = p == 0.f ? 0.f : p * wv[hf];
-          }
-          const __half2 hi = __floats2half2_rn(w[0], w[1]);
-          const float2 back = __half22float2(hi);
-          ph[n][hf] = transpose8x8(h2_bits(hi));
-          pl[n][hf] = transpose8x8(h2_bits(__floats2half2_rn(w[0] - back.x, w[1] - back.y)));
-        }
-      // ---- O^T += V_int^T w: dims 16 g + 2 i + {0, 1} in m-tile i
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t va[8], vb[8];             // 8 dims of key pairs (2t, 2t+1) and (2t+8, 2t+9)
-#pragma unroll
-        for (int pr = 0; pr < 2; ++pr) {
-          uint32_t(&dst)[8] = pr ? vb : va;
-          if (BITS == 4) {
-            const uint32_t a = half ? vf[2 * pr].c[0].y : vf[2 * pr].c[0].x;
-            const uint32_t bb = half ? vf[2 * pr + 1].c[0].y : vf[2 * pr + 1].c[0].x;
-            uint32_t x[4];
-#pragma unroll
-            for (int hw = 0; hw < 2; ++hw) {
-              const uint32_t mix = __byte_perm(a, bb, hw ? 0x7632u : 0x5410u);
-              const __half2 six = __float2half2_rn(0.0625f);
-              const uint32_t m8 = mix >> 8;
-              x[0] = h2_bits(__hadd2(bits_h2((mix & 0x000F000Fu) | 0x64006400u), vz1[pr]));
-              x[1] = h2_bits(__hfma2(bits_h2((mix & 0x00F000F0u) | 0x64006400u), six, vz16[pr]));
-              x[2] = h2_bits(__hadd2(bits_h2((m8 & 0x000F000Fu) | 0x64006400u), vz1[pr]));
-              x[3] = h2_bits(__hfma2(bits_h2((m8 & 0x00F000F0u) | 0x64006400u), six, vz16[pr]));
-#pragma unroll
-              for (int e = 0; e < 4; ++e) dst[4 * hw + e] = x[e];
-            }
-          } else {
-            const uint2 a2 = vf[2 * pr].c[BITS == 4 ? 0 : half];
-            const uint2 b2 = vf[2 * pr + 1].c[BITS == 4 ? 0 : half];
-#pragma unroll
-            for (int hw = 0; hw < 2; ++hw) {
-              const uint32_t a = hw ? a2.y : a2.x, bb = hw ? b2.y : b2.x;
-              const uint32_t lo = __byte_perm(a, bb, 0x5140u), hi = __byte_perm(a, bb, 0x7362u);
-              uint32_t x[2], y[2];
-              widen_bytes(lo, vz1[pr], x);
-              widen_bytes(hi, vz1[pr], y);
-              dst[4 * hw] = x[0], dst[4 * hw + 1] = x[1];
-              dst[4 * hw + 2] = y[0], dst[4 * hw + 3] = y[1];
-            }
-          }
-        }
-#pragma unroll
-        for (int i4 = 0; i4 < 4; ++i4) {
-          const uint32_t a[4] = {va[2 * i4], va[2 * i4 + 1], vb[2 * i4], vb[2 * i4 + 1]};
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma16816(o[n][4 * half + i4], a, ph[n][0], ph[n][1]);
-            mma16816(o[n][4 * half + i4], a, pl[n][0], pl[n][1]);
-          }
-        }
-      }
+      fetch(i + DEPTH, page_next, slot);
+      page_next = page_of(i + DEPTH + 1);
     }
+    cp_async_wait<0>();
 
     // ---- the warps' results into shared memory, at a common maximum
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
+        const int r = 8 * n + 2 * t + c;
 #pragma unroll
-        for (int of = 4; of < 32; of <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], of);
-        if (g == 0) {
-          sm_m[warp][8 * n + 2 * t + c] = m[n][c];
-          sm_l[warp][8 * n + 2 * t + c] = l[n][c];
+        for (int of = 4; of < 32; of <<= 1) {
+          l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], of);
+        }
+        if (g == 0 && r < R) {
+          sm_m[warp][r] = m[n][c];
+          sm_l[warp][r] = l[n][c];
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float2*>(&sm_o[warp][8 * n + 2 * t + c][16 * g + 2 * i]) =
-              make_float2(o[n][i][c] * svr, o[n][i][2 + c] * svr);
+        for (int i = 0; i < 8; ++i) {
+          float x = o[n][i][c], y = o[n][i][2 + c];
+          if (PAIR) {                      // the low parts' columns
+            x += __shfl_down_sync(0xffffffffu, x, 2);
+            y += __shfl_down_sync(0xffffffffu, y, 2);
+          }
+          x = x * 16777216.0f * svr;
+          y = y * (BITS == 4 ? 1048576.0f : 16777216.0f) * svr;
+          if (r < R) *reinterpret_cast<float2*>(&sm_o[warp][r][16 * g + 2 * i]) = make_float2(x, y);
+        }
       }
     __syncthreads();
     // thread tid owns dim tid of every row
-    const int64_t c0 = ((u0 + 1) * ctas - 1) / total;            // CTA that holds the unit's first tile
-    const int64_t c1 = ((u0 + per) * ctas - 1) / total;          // and its last
-    const int slot = 2 * blockIdx.x + (u0 >= r0 ? 1 : 0);
+    const int part = 2 * blockIdx.x + (u0 >= r0 ? 1 : 0);
     constexpr int PART = R * (D + 2);
     float acc[R], mm[R], ll[R];
 #pragma unroll
@@ -478,8 +607,62 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 3) stream_kernel(const 
       }
     }
     bool finish = whole;
+    // adds n pieces (ml(j, r): reference and sum; o(j, r): this thread's dim) to (acc, mm, ll): the
+    // largest reference first, then 128 / R pieces' factors at a time by one thread each, so that
+    // every load but the factors' is independent
+    auto join = [&](int n, auto ml, auto out) {
+      constexpr int STEP = THREADS / R, AHEAD = 32 / R;
+      const int jr = tid % R, jq = tid / R;
+      float top = -INFINITY;
+      for (int q = jq; q < n; q += STEP) top = fmaxf(top, ml(q, jr).x);
+      sm_f[tid] = top;
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float x = mm[r];
+        for (int k = 0; k < STEP; ++k) x = fmaxf(x, sm_f[k * R + r]);
+        const float f = mm[r] == -INFINITY ? 0.f : ex2(mm[r] - x);
+        acc[r] = f != 0.f ? acc[r] * f : 0.f;
+        ll[r] *= f;
+        mm[r] = x;
+        if (tid == r) sm_top[r] = x;
+      }
+      for (int q0 = 0; q0 < n; q0 += STEP) {
+        __syncthreads();
+        const int q = q0 + jq;
+        float f = 0.f, fl = 0.f;
+        if (q < n) {
+          const float2 v = ml(q, jr);
+          f = v.x == -INFINITY ? 0.f : ex2(v.x - sm_top[jr]);
+          fl = f * v.y;
+        }
+        sm_f[tid] = f;
+        sm_fl[tid] = fl;
+        __syncthreads();
+        const int cnt = min(STEP, n - q0);
+        for (int k0 = 0; k0 < cnt; k0 += AHEAD) {
+          float po[AHEAD][R];
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+            for (int r = 0; r < R; ++r) po[k][r] = out(q0 + min(k0 + k, cnt - 1), r);
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k)
+            if (k0 + k < cnt) {
+#pragma unroll
+              for (int r = 0; r < R; ++r) {
+                const float w = sm_f[(k0 + k) * R + r];
+                if (w != 0.f) acc[r] = fmaf(w, po[k][r], acc[r]);
+                ll[r] += sm_fl[(k0 + k) * R + r];
+              }
+            }
+        }
+      }
+      __syncthreads();
+    };
     if (!whole) {
-      float* p = P.part + static_cast<int64_t>(slot) * PART;
+      const int64_t c0 = u0 / piece, c1 = (u0 + per - 1) / piece;      // CTAs of its first and last tile
+      float* p = P.part + static_cast<int64_t>(part) * PART;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         p[r * D + tid] = acc[r];
@@ -501,44 +684,43 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 3) stream_kernel(const 
         __threadfence();
 #pragma unroll
         for (int r = 0; r < R; ++r) mm[r] = -INFINITY, ll[r] = acc[r] = 0.f;
-        for (int64_t c = c0; c <= c1; ++c) {
-          const int64_t cb = total * c / ctas;
-          const float* p2 = P.part + (2 * c + (u0 >= cb ? 1 : 0)) * PART;
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float pm = __ldcg(p2 + R * D + r), plv = __ldcg(p2 + R * D + R + r);
-            const float M = fmaxf(mm[r], pm);
-            const float fa = mm[r] == -INFINITY ? 0.f : ex2(mm[r] - M);
-            const float fb = pm == -INFINITY ? 0.f : ex2(pm - M);
-            const float po = __ldcg(p2 + r * D + tid);
-            acc[r] = fa * acc[r] + (fb != 0.f ? fb * po : 0.f);
-            ll[r] = fa * ll[r] + fb * plv;
-            mm[r] = M;
-          }
-        }
+        auto place = [&](int j) {
+          const int64_t c = c0 + j;
+          return P.part + (2 * c + (u0 >= c * piece ? 1 : 0)) * PART;
+        };
+        join(static_cast<int>(c1 - c0) + 1,
+             [&](int j, int r) {
+               const float* p = place(j) + R * D + r;
+               return make_float2(__ldcg(p), __ldcg(p + R));
+             },
+             [&](int j, int r) { return __ldcg(place(j) + r * D + tid); });
       }
     }
     if (finish) {
+      int64_t row[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int rr = min(r, u.rows - 1), tok = (u.row0 + rr) / G;
+        row[r] = static_cast<int64_t>(u.s.row0 + tok) * P.hq + u.h * G + u.row0 + rr - tok * G;
+      }
+      if (P.ex_n > 0) {
+        // the shared prefix's part of the rows, in pieces
+        const int64_t step = P.batch.T * P.hq;
+        join(P.ex_n,
+             [&](int j, int r) {           // r is not known to the compiler here
+               const int rr = min(r, u.rows - 1), tok = (u.row0 + rr) / G;
+               const int64_t at = static_cast<int64_t>(u.s.row0 + tok) * P.hq + u.h * G + u.row0 + rr - tok * G;
+               return __ldcg(reinterpret_cast<const float2*>(P.ex_ml) + j * step + at);
+             },
+             [&](int j, int r) { return __ldcg(P.ex_o + (j * step + row[r]) * D + tid); });
+      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (r < u.rows) {
-          const int tok = (u.row0 + r) / G, head = u.h * G + u.row0 + r - tok * G;
-          const int64_t row = static_cast<int64_t>(u.s.row0 + tok) * P.hq + head;
-          // the shared prefix's part of the row, in pieces
-          for (int e = 0; e < P.ex_n; ++e) {
-            const int64_t at = static_cast<int64_t>(e) * P.batch.T * P.hq + row;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(P.ex_ml) + at);
-            const float po = __ldcg(P.ex_o + at * D + tid);
-            const float M = fmaxf(mm[r], ml.x);
-            const float fa = mm[r] == -INFINITY ? 0.f : ex2(mm[r] - M);
-            const float fb = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-            acc[r] = fa * acc[r] + (fb != 0.f ? fb * po : 0.f);
-            ll[r] = fa * ll[r] + fb * ml.y;
-            mm[r] = M;
-          }
           const float y = ll[r] == 0.f ? 0.f : acc[r] / ll[r];
-          P.out[row * D + tid] = __float2bfloat16_rn(y);
-          if (P.lse && tid == r) P.lse[row] = ll[r] == 0.f ? -INFINITY : (mm[r] + log2f(ll[r])) * kLn2;
+          P.out[row[r] * D + tid] = __float2bfloat16_rn(y);
+          if (P.lse && tid == r)
+            P.lse[row[r]] = ll[r] == 0.f ? -INFINITY : (mm[r] + log2f(ll[r])) * kLn2;
         }
       }
     }
@@ -553,26 +735,40 @@ namespace {
 constexpr size_t kCountBytes = 16384;
 constexpr int kMaxGrid = kCountBytes / 4;
 
-template <int BITS, int NT>
-int grid_size() {
-  static int cache[64] = {0};
-  const int d = host::current_device();
-  if (d >= 0 && d < 64 && cache[d] > 0) return cache[d];
+using StreamFn = void (*)(AttnParams);
+struct StreamKernel {
+  StreamFn fn;
+  int rows, smem;
+};
+
+// kind: 0 up to 4 rows a unit, 1 up to 8, 2 up to 16.
+template <int BITS>
+StreamKernel stream_variant(int kind) {
+  if (kind == 0) return {stream_kernel<BITS, 1, true>, 4, Stream<BITS, 1, true>::SMEM};
+  if (kind == 1) return {stream_kernel<BITS, 1, false>, 8, Stream<BITS, 1, false>::SMEM};
+  return {stream_kernel<BITS, 2, false>, 16, Stream<BITS, 2, false>::SMEM};
+}
+StreamKernel stream_of(int bits, int kind) {
+  return bits == 4 ? stream_variant<4>(kind) : stream_variant<8>(kind);
+}
+
+// CTAs that the device holds at once; the first call on a device also allows the kernel its
+// shared memory.
+int stream_grid(int bits, int kind) {
+  static std::atomic<int> cache[64][6];
+  const int d = host::current_device(), v = kind + (bits == 4 ? 0 : 3);
+  if (d >= 0 && d < 64 && cache[d][v].load() > 0) return cache[d][v].load();
+  const StreamKernel k = stream_of(bits, kind);
   int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stream_kernel<BITS, NT>, THREADS, 0) !=
-          cudaSuccess ||
+  if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k.fn, THREADS, k.smem) != cudaSuccess ||
       per_sm < 1) {
     (void)cudaGetLastError();
     per_sm = 1;
   }
   const int grid = host::num_sms() * per_sm < kMaxGrid ? host::num_sms() * per_sm : kMaxGrid;
-  if (d >= 0 && d < 64) cache[d] = grid;
+  if (d >= 0 && d < 64) cache[d][v].store(grid);
   return grid;
-}
-
-int any_grid(int bits, int nt) {
-  if (bits == 4) return nt == 1 ? grid_size<4, 1>() : grid_size<4, 2>();
-  return nt == 1 ? grid_size<8, 1>() : grid_size<8, 2>();
 }
 
 // Sequences of up to this many rows (new tokens x query heads per KV head)
@@ -589,7 +785,7 @@ AttnPlan make_plan(int64_t T, int hq, int hkv, int B, int max_q, int64_t keys, i
   AttnPlan p{};
   const int64_t G = hq / hkv, rows = G * max_q;
   const int sms = host::num_sms();
-  p.nt = rows <= 8 ? 1 : 2;
+  p.kind = rows <= 4 ? 0 : rows <= 8 ? 1 : 2;
   p.shared = prefix_len > 0 && rows <= kSharedRows && B > 1 && have_ws;
   p.tile = !p.shared && rows > kFewRows;
   p.stream = p.shared || !p.tile || B > 1;
@@ -601,7 +797,7 @@ AttnPlan make_plan(int64_t T, int hq, int hkv, int B, int max_q, int64_t keys, i
     return o;
   };
   if (p.stream)
-    p.part = take(static_cast<size_t>(any_grid(bits, p.nt)) * 2 * (8 * p.nt) * (D + 2) * 4);
+    p.part = take(static_cast<size_t>(stream_grid(bits, p.kind)) * 2 * stream_of(bits, p.kind).rows * (D + 2) * 4);
   if (p.shared) {
     const int64_t units = (T * G + kTileRows - 1) / kTileRows * hkv, tiles = (prefix_len + 127) / 128;
     int64_t s = sms / units;
@@ -679,10 +875,9 @@ sq_status run_attention(const void* q, int64_t q_stride, int64_t T, int hq,
   }
   if (!plan.stream) return SQ_OK;
   P.ex_n = plan.shared ? plan.tile_split : 0;
-  const int grid = any_grid(pages.bits, plan.nt);
-  auto kern = pages.bits == 4 ? (plan.nt == 1 ? stream_kernel<4, 1> : stream_kernel<4, 2>)
-                              : (plan.nt == 1 ? stream_kernel<8, 1> : stream_kernel<8, 2>);
-  kern<<<grid, THREADS, 0, stream>>>(P);
+  const int grid = stream_grid(pages.bits, plan.kind);
+  const StreamKernel k = stream_of(pages.bits, plan.kind);
+  k.fn<<<grid, THREADS, k.smem, stream>>>(P);
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SQ_OK : host::cuda_fail("kv attention launch", e);
 }

@@ -128,7 +128,7 @@ __device__ __forceinline__ void widen_bytes(uint32_t w, __half2 z1, uint32_t (&o
 
 // What a call launches and the workspace it wants (kv_attend.cu).
 struct AttnPlan {
-  int nt;                                  // streaming kernel: 8-row blocks per unit
+  int kind;                                // streaming kernel: up to 4, 8 or 16 rows per unit
   bool stream, tile, shared;               // which kernels run; shared: the prefix pass
   int tile_split;                          // CTAs that may share a tile unit
   int64_t tile_units;
