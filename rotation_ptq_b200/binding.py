@@ -6,7 +6,6 @@ goes straight to the matching ``sq_*`` entry point on torch's current stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -141,7 +140,9 @@ def version() -> int:
 
 
 def _stream(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+    # what torch.cuda.current_stream(t.device).cuda_stream says, without the Stream object (1.5 us of
+    # a call that takes 10)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _ptr(t):
@@ -165,16 +166,22 @@ def _expect(t, name, dtype, shape):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.dtype != dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
 
 
 def _same_device(*ts):
-    devs = {t.device for t in ts if t is not None}
-    if len(devs) > 1:
-        raise ValueError("all tensors must be on one device, got %s" % sorted(map(str, devs)))
+    first = None
+    for t in ts:
+        if t is None:
+            continue
+        if first is None:
+            first = t.device
+        elif t.device != first:
+            devs = {t.device for t in ts if t is not None}
+            raise ValueError("all tensors must be on one device, got %s" % sorted(map(str, devs)))
 
 
 def _expect_workspace(ws):
@@ -643,6 +650,7 @@ class KVPages:
         self._struct = _PagesStruct(*(t.data_ptr() for t in self._tensors), n, ps, hkv, 128,
                                     self.bits)
         self._ref = ctypes.addressof(self._struct)
+        self._ws_bytes = {}                  # workspace bytes by a call's sizes
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, hkv: int, bits: int = 4, device=None):
@@ -690,11 +698,12 @@ def _expect_batch(pages, block_table, cu_seqlens, lengths, lname):
     return B, width
 
 
-def _on_device(device):
-    """Makes `device` current around a C call (the library launches on the current device)."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _call_on(device_index, fn, *args):
+    """fn(*args) with the device current (the library launches on the current device)."""
+    if device_index == torch._C._cuda_getDevice():
+        return fn(*args)
+    with torch.cuda.device(device_index):
+        return fn(*args)
 
 
 def kv_paged_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pages: KVPages,
@@ -742,12 +751,11 @@ def kv_paged_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pages: KV
     _need_cuda(q, pages.k_codes)
     if q_out is None:
         q_out = torch.empty((T, hq, 128), dtype=torch.bfloat16, device=q.device)
-    with _on_device(q.device):
-        st = lib.sq_kv_paged_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), sq_, sk, sv, T, hq,
-                                    pages._ref, block_table.data_ptr(), width,
-                                    cu_seqlens.data_ptr(), cached.data_ptr(), B, _ptr(cos),
-                                    _ptr(sin), max_pos, rot, int(bool(interleaved)), _ptr(q_norm),
-                                    _ptr(k_norm), float(eps), q_out.data_ptr(), _stream(q))
+    st = _call_on(q.get_device(), lib.sq_kv_paged_append, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                  sq_, sk, sv, T, hq, pages._ref, block_table.data_ptr(), width,
+                  cu_seqlens.data_ptr(), cached.data_ptr(), B, _ptr(cos), _ptr(sin), max_pos, rot,
+                  int(bool(interleaved)), _ptr(q_norm), _ptr(k_norm), float(eps), q_out.data_ptr(),
+                  _stream(q))
     _check(st, "sq_kv_paged_append")
     return q_out
 
@@ -771,10 +779,9 @@ def kv_paged_dequant(pages: KVPages, block_table: torch.Tensor, cu_seqlens: torc
         k_out = torch.empty(shape, dtype=torch.bfloat16, device=pages.device)
     if v_out is None:
         v_out = torch.empty(shape, dtype=torch.bfloat16, device=pages.device)
-    with _on_device(pages.device):
-        st = lib.sq_kv_paged_dequant(pages._ref, block_table.data_ptr(), width,
-                                     cu_seqlens.data_ptr(), cached.data_ptr(), B, shape[0],
-                                     k_out.data_ptr(), v_out.data_ptr(), _stream(block_table))
+    st = _call_on(block_table.get_device(), lib.sq_kv_paged_dequant, pages._ref,
+                  block_table.data_ptr(), width, cu_seqlens.data_ptr(), cached.data_ptr(), B,
+                  shape[0], k_out.data_ptr(), v_out.data_ptr(), _stream(block_table))
     _check(st, "sq_kv_paged_dequant")
     return k_out, v_out
 
@@ -834,7 +841,7 @@ def kv_prefix_attention(q: torch.Tensor, pages: KVPages, prefix_table: torch.Ten
 def _attention_workspace(device, stream, need):
     # a graph gets a workspace of its own, zeroed by the graph: a cached one
     # would be shared by graphs that may replay at the same time
-    if torch.cuda.is_current_stream_capturing():
+    if torch._C._cuda_isCurrentStreamCapturing():
         return torch.zeros((need,), dtype=torch.uint8, device=device)
     key = (device.index, stream, "attention")
     with _ws_lock:
@@ -867,22 +874,30 @@ def _kv_attention(q, pages, prefix_table, prefix_len, block_table, cu_seqlens, l
     rule = _ScoreRule(128 ** -0.5 if scale is None else float(scale), float(softcap), int(window),
                       _ptr(slopes))
     max_q = int(max_q)
-    with _on_device(q.device):
-        stream = _stream(q)
-        if workspace is None:
-            need = kv_attention_workspace_bytes(T, hq, pages, B, width, max_q, prefix_len)
-            workspace = _attention_workspace(q.device, stream, need) if need else None
-        ws_ptr = None if workspace is None else workspace.data_ptr()
-        ws_bytes = 0 if workspace is None else workspace.numel()
-        args = (block_table.data_ptr(), width, cu_seqlens.data_ptr(), lengths.data_ptr(), B, max_q,
-                ctypes.addressof(rule), out.data_ptr(), _ptr(lse), ws_ptr, ws_bytes, stream)
-        if prefix_table is None:
-            st = lib.sq_kv_paged_attention(q.data_ptr(), stride, T, hq, pages._ref, *args)
-            name = "sq_kv_paged_attention"
-        else:
-            st = lib.sq_kv_prefix_attention(q.data_ptr(), stride, T, hq, pages._ref,
-                                            prefix_table.data_ptr(), prefix_len, *args)
-            name = "sq_kv_prefix_attention"
+    device = q.get_device()
+    stream = _stream(q)
+    if workspace is None:
+        sizes = (T, hq, B, width, max_q, prefix_len)
+        need = pages._ws_bytes.get(sizes)
+        if need is None:
+            need = _call_on(device, kv_attention_workspace_bytes, T, hq, pages, B, width, max_q,
+                            prefix_len)
+            if len(pages._ws_bytes) >= 4096:
+                pages._ws_bytes.clear()
+            pages._ws_bytes[sizes] = need
+        workspace = _call_on(device, _attention_workspace, q.device, stream, need) if need else None
+    ws_ptr = None if workspace is None else workspace.data_ptr()
+    ws_bytes = 0 if workspace is None else workspace.numel()
+    args = (block_table.data_ptr(), width, cu_seqlens.data_ptr(), lengths.data_ptr(), B, max_q,
+            ctypes.addressof(rule), out.data_ptr(), _ptr(lse), ws_ptr, ws_bytes, stream)
+    if prefix_table is None:
+        st = _call_on(device, lib.sq_kv_paged_attention, q.data_ptr(), stride, T, hq, pages._ref,
+                      *args)
+        name = "sq_kv_paged_attention"
+    else:
+        st = _call_on(device, lib.sq_kv_prefix_attention, q.data_ptr(), stride, T, hq, pages._ref,
+                      prefix_table.data_ptr(), prefix_len, *args)
+        name = "sq_kv_prefix_attention"
     _check(st, name)
     return out
 

@@ -2,7 +2,7 @@
 // sm_100a: the streaming kernel.
 //
 // With rows = (new tokens) x (query heads per KV head) of one KV head, this
-// kernel computes, over tiles of 64 keys (16 per warp),
+// kernel computes, over tiles of 128 keys (32 per warp and step),
 //     S^T = C_k Q^T,   s = (S - z_k sum q) sk f_row,   w = exp2(s - m) sv,
 //     O^T += (C_v - z_v)^T w
 // with C the codes as they are stored, z the zero points and sk, sv the row
@@ -101,12 +101,14 @@ template <int BITS, int NT, bool PAIR>
 struct Stream {
   static constexpr int R = PAIR ? 4 : 8 * NT;            // rows per unit
   static constexpr int RB = D * BITS / 8;
-  static constexpr int DEPTH = BITS == 4 ? 4 : 3;        // ring slots per warp
-  // a slot: 16 keys' K codes, V codes, K scales, V scales, K zero points, V zero points
-  static constexpr int V0 = 16 * RB, SC0 = 32 * RB, SLOT = 32 * RB + 160;
+  static constexpr int DEPTH = 2;                        // ring slots per warp
+  // a slot: two groups of 16 keys, each K codes, V codes, K scales, V scales, K zero points,
+  // V zero points; behind a unit's keys the ring holds the warp's sums
+  static constexpr int V0 = 16 * RB, SC0 = 32 * RB, GROUP = 32 * RB + 160, SLOT = 2 * GROUP;
   static constexpr int RING = DEPTH * SLOT;
-  static constexpr int SMEM = WARPS * (RING + R * D * 4);
-  static constexpr int CTAS = NT == 1 ? (BITS == 4 ? 4 : 3) : 3;
+  static constexpr int SMEM = WARPS * RING;
+  static_assert(R * D * 4 <= RING, "sums in the ring");
+  static constexpr int CTAS = NT == 1 ? 3 : 2;
 
   // Where 16-byte chunk c of key row r lies: rows are permuted inside 128-byte lines so that the
   // lanes of a load phase, two keys apart (V) or one (K), do not share banks.
@@ -151,8 +153,12 @@ struct Stream {
       // 2^(14 - floor(log2 mx)), its exponent kept inside float32's
       const int ex = static_cast<int>((__float_as_uint(mx) >> 23) & 0xFFu) - 127;
       const int up = mx > 0.f ? max(-126, min(126, 14 - ex)) : 0;
-      const float f = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+      float f = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
       const float inv = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+      // a factor >= 0 lets the maximum be taken before it is applied
+      float mine = inv * 16777216.0f * P.scale * (P.cap > 0.f ? 1.0f / P.cap : kLog2e);
+      if (mine < 0.f) mine = -mine, f = -f;
+      if (mine == 0.f) mine = 1.f, f = 0.f;
       // 4-bit codes of the second register of a pair are 16 n 2^-24
       const float fb = BITS == 4 ? f * 0.0625f : f;
       float sum = 0.f;
@@ -172,7 +178,6 @@ struct Stream {
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       sum *= 5.9604645e-08f;               // codes are n 2^-24
       // the factor of row 8 n + g lives in its lanes; columns 2t, 2t + 1 need rows 2t, 2t + 1
-      const float mine = inv * 16777216.0f * P.scale * (P.cap > 0.f ? 1.0f / P.cap : kLog2e);
       qs[n][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
       qs[n][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
       qf[n][0] = __shfl_sync(0xffffffffu, mine, 8 * t);
@@ -186,7 +191,7 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
   using St = Stream<BITS, NT, PAIR>;
   constexpr int R = St::R, RB = St::RB, DEPTH = St::DEPTH;
   extern __shared__ __align__(128) uint8_t stream_smem[];
-  float(*sm_o)[R][D] = reinterpret_cast<float(*)[R][D]>(stream_smem + WARPS * St::RING);
+  auto sm_o = [&](int w) { return reinterpret_cast<float(*)[D]>(stream_smem + w * St::RING); };
   __shared__ float sm_m[WARPS][R], sm_l[WARPS][R], sm_f[THREADS], sm_fl[THREADS], sm_top[R];
   __shared__ int64_t sm_scan[WARPS];
   __shared__ int64_t sm_total, sm_base;
@@ -265,68 +270,6 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
     cur += i1 - i0;
     const int first = split ? i0 : 0, last = split ? min(i1, u.s.tiles()) : u.s.tiles();
 
-    // ---- where the warp's keys of tile i are, and their way into the ring
-    const uint8_t* ring = stream_smem + warp * St::RING;
-    const uint32_t ring32 = smem_u32(ring);
-    struct Keys {
-      int local, limit, kpos;              // first row of 16, rows of its pages, position of the first
-      const int32_t* table;
-    };
-    auto keys_of = [&](int i) {
-      const bool pre = i < u.s.pn;
-      Keys k;
-      k.local = (pre ? u.s.pt0 + i : u.s.ot0 + i - u.s.pn) * TILE + 16 * warp;
-      k.limit = pre ? P.prefix_len : u.s.len;
-      k.kpos = (pre ? 0 : P.prefix_len) + k.local;
-      k.table = pre ? P.prefix_table : P.batch.table + static_cast<int64_t>(u.b) * P.batch.width;
-      return k;
-    };
-    auto page_of = [&](int i) {            // -1: no keys
-      if (i >= last) return -1;
-      const Keys k = keys_of(i);
-      return k.local < k.limit ? k.table[k.local >> P.pages.lps] : -1;
-    };
-    unsigned filled = 0;                   // bit slot: it holds keys
-    // lanes 0..3 fetch the K scales, 4..7 the V scales, 8 and 9 the zero points
-    const uint8_t* extra = reinterpret_cast<const uint8_t*>(lane < 4 ? P.pages.ks : P.pages.vs) + 16 * (lane & 3);
-    if (lane == 8) extra = P.pages.kz;
-    if (lane == 9) extra = P.pages.vz;
-    const int extra_step = lane < 8 ? 4 : 1;
-    auto fetch = [&](int i, int page, int slot) {
-      filled &= ~(1u << slot);
-      if (i < last) {
-        const Keys k = keys_of(i);
-        if (k.local < k.limit) {
-          if (page < 0 || page >= P.pages.num_pages) {
-            if (lane == 0) record_status(SQ_ERR_INVALID_ARG);
-          } else {
-            const int64_t grp = group_of(P.pages, page, u.h, k.local & ((1 << P.pages.lps) - 1));
-            const uint32_t dst = ring32 + slot * St::SLOT;
-            const uint8_t* kc = P.pages.kc + grp * RB + 16 * lane;
-            const uint8_t* vc = P.pages.vc + grp * RB + 16 * lane;
-            constexpr int CPR = RB / 16, RPI = 32 / CPR;         // chunks per row, rows per instruction
-#pragma unroll
-            for (int j = 0; j < 16 / RPI; ++j) {
-              const int r = j * RPI + lane / CPR, c = lane % CPR;
-              cp_async16(dst + St::k_at(r, c), kc + 512 * j);
-              cp_async16(dst + St::V0 + St::v_at(r, c), vc + 512 * j);
-            }
-            if (lane < 10) cp_async16(dst + St::SC0 + 16 * lane, extra + grp * extra_step);
-            filled |= 1u << slot;
-          }
-        }
-      }
-      cp_async_commit();
-    };
-    {
-      int pages[DEPTH];
-#pragma unroll
-      for (int d = 0; d < DEPTH; ++d) pages[d] = page_of(first + d);
-#pragma unroll
-      for (int d = 0; d < DEPTH; ++d) fetch(first + d, pages[d], d);
-    }
-    int page_next = page_of(first + DEPTH);
-
     uint32_t qb[NT][8][2];
     float qf[NT][2], qs[NT][2];
     St::load_q(P, u, g, t, qb, qf, qs);
@@ -354,212 +297,301 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
       m[n][0] = m[n][1] = -INFINITY;
       l[n][0] = l[n][1] = 0.f;
     }
+    const bool special = P.cap > 0.f || P.slopes != nullptr;
+    float ff[NT][2];                       // the scores' factor inside the exponential
+#pragma unroll
+    for (int n = 0; n < NT; ++n) ff[n][0] = special ? 1.f : qf[n][0], ff[n][1] = special ? 1.f : qf[n][1];
     float svr = 0.f, svi = 0.f;            // power of two at or above the value scales so far; 1 / svr
 
-    int slot = 0;
-    for (int i = first; i < last; ++i, slot = slot + 1 == DEPTH ? 0 : slot + 1) {
-      cp_async_wait<DEPTH - 1>();
-      __syncwarp();
-      if ((filled >> slot) & 1u) {
-        const uint8_t* sl = ring + slot * St::SLOT;
-        const Keys k = keys_of(i);
-        float sk[2], sv[2], kz[2];
-        uint32_t vz[2];                    // less the zero points of keys 2t, 2t + 1 (+ 8): fp16 -z 2^-24
+    const uint8_t* ring = stream_smem + warp * St::RING;
+    const uint32_t ring32 = smem_u32(ring);
+    // lanes 0..3 fetch a group's K scales, 4..7 its V scales, 8 and 9 its zero points
+    const uint8_t* extra = reinterpret_cast<const uint8_t*>(lane < 4 ? P.pages.ks : P.pages.vs) + 16 * (lane & 3);
+    if (lane == 8) extra = P.pages.kz;
+    if (lane == 9) extra = P.pages.vz;
+    const int extra_step = lane < 8 ? 4 : 1;
+    const int in_page = (1 << P.pages.lps) - 1;
+
+    // the shared prefix's tiles that are this CTA's (where no other kernel takes them), then the own
+#pragma unroll 1
+    for (int seg = first < u.s.pn ? 0 : 1; seg < 2; ++seg) {
+      const int t0 = seg ? u.s.ot0 + max(first - u.s.pn, 0) : u.s.pt0 + first;
+      const int t1 = seg ? u.s.ot0 + last - u.s.pn : u.s.pt0 + min(last, u.s.pn);
+      const int limit = seg ? u.s.len : P.prefix_len, kshift = seg ? P.prefix_len : 0;
+      const int32_t* table = seg ? P.batch.table + static_cast<int64_t>(u.b) * P.batch.width : P.prefix_table;
+      const int end = min(limit, t1 * TILE);
+      // ---- the way of 32 keys into the ring; pages of both groups, -1: no keys
+      auto pages_of = [&](int local, int (&pg)[2]) {
+        pg[0] = local < end ? __ldg(table + (local >> P.pages.lps)) : -1;
+        pg[1] = local + 16 < end ? __ldg(table + ((local + 16) >> P.pages.lps)) : -1;
+      };
+      unsigned there = 0;                  // bits 2 slot + group: it holds keys
+      auto fetch = [&](int local, const int (&pg)[2], int slot) {
+        there &= ~(3u << (2 * slot));
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const uint8_t* x = sl + St::SC0;
-          sk[hf] = reinterpret_cast<const float*>(x)[g + 8 * hf];
-          sv[hf] = reinterpret_cast<const float*>(x)[16 + g + 8 * hf];
-          kz[hf] = static_cast<float>(x[128 + g + 8 * hf]);
-          const uint32_t zz = reinterpret_cast<const uint16_t*>(x + 144)[t + 4 * hf];
-          vz[hf] = __byte_perm(zz, 0u, 0x4140u) | 0x80008000u;
-        }
-        // ---- S^T = C_k Q^T
-        float sc[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
-#pragma unroll
-        for (int c = 0; c < BITS / 4; ++c) {
-          const uint4 a4 = *reinterpret_cast<const uint4*>(sl + St::k_at(g, t + 4 * c));
-          const uint4 b4 = *reinterpret_cast<const uint4*>(sl + St::k_at(g + 8, t + 4 * c));
-          const uint32_t wa[4] = {a4.x, a4.y, a4.z, a4.w}, wb[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            if (BITS == 4) {
-              const uint32_t a8 = wa[w] >> 8, b8 = wb[w] >> 8;
-              const uint32_t f0[4] = {wa[w] & 0x000F000Fu, wb[w] & 0x000F000Fu, wa[w] & 0x00F000F0u,
-                                      wb[w] & 0x00F000F0u};
-              const uint32_t f1[4] = {a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u,
-                                      b8 & 0x00F000F0u};
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                mma16816(sc[n], f0, qb[n][2 * w][0], qb[n][2 * w][1]);
-                mma16816(sc[n], f1, qb[n][2 * w + 1][0], qb[n][2 * w + 1][1]);
-              }
+        for (int gr = 0; gr < 2; ++gr) {
+          const int row = local + 16 * gr;
+          if (row < end) {
+            if (pg[gr] < 0 || pg[gr] >= P.pages.num_pages) {
+              if (lane == 0) record_status(SQ_ERR_INVALID_ARG);
             } else {
-              const uint32_t f0[4] = {__byte_perm(wa[w], 0u, 0x4140u), __byte_perm(wb[w], 0u, 0x4140u),
-                                      __byte_perm(wa[w], 0u, 0x4342u), __byte_perm(wb[w], 0u, 0x4342u)};
+              const int64_t grp = group_of(P.pages, pg[gr], u.h, row & in_page);
+              const uint32_t dst = ring32 + slot * St::SLOT + gr * St::GROUP;
+              const uint8_t* kc = P.pages.kc + grp * RB + 16 * lane;
+              const uint8_t* vc = P.pages.vc + grp * RB + 16 * lane;
+              constexpr int CPR = RB / 16, RPI = 32 / CPR;       // chunks per row, rows per instruction
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816(sc[n], f0, qb[n][4 * c + w][0], qb[n][4 * c + w][1]);
+              for (int j = 0; j < 16 / RPI; ++j) {
+                const int rw = j * RPI + lane / CPR, c = lane % CPR;
+                cp_async16(dst + St::k_at(rw, c), kc + 512 * j);
+                cp_async16(dst + St::V0 + St::v_at(rw, c), vc + 512 * j);
+              }
+              if (lane < 10) cp_async16(dst + St::SC0 + 16 * lane, extra + grp * extra_step);
+              there |= 1u << (2 * slot + gr);
             }
           }
         }
-        // ---- scores: [n][0], [1] key g; [2], [3] key g + 8; columns 2t, 2t + 1
-        const bool plain = P.cap <= 0.f && P.slopes == nullptr && k.local + 16 <= k.limit &&
-                           k.kpos + 15 <= qmin && (P.window == 0 || qmax - k.kpos < P.window);
-        bool raise = false;
-        float svmax = 0.f;
+        cp_async_commit();
+      };
+      int local = t0 * TILE + 32 * warp;
+      int pg[2], pn[2];
+      pages_of(local, pg);
+      pages_of(local + TILE, pn);
+      fetch(local, pg, 0);
+      fetch(local + TILE, pn, 1);
+      pages_of(local + 2 * TILE, pg);
+
+      for (int slot = 0; local < end; local += TILE, slot ^= 1) {
+        cp_async_wait<St::DEPTH - 1>();
+        __syncwarp();
+        const unsigned have = (there >> (2 * slot)) & 3u;
+        if (have) {
+          const uint8_t* sl = ring + slot * St::SLOT;
+          const int kpos = kshift + local;
+          // ---- S^T = C_k Q^T: [group][n][0], [1] key g; [2], [3] key g + 8; columns 2t, 2t + 1
+          float sc[2][NT][4], sk[2][2], sv[2][2], kz[2][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int gr = 0; gr < 2; ++gr) {
+            const uint8_t* x = sl + gr * St::GROUP;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            sc[n][e] = fmaf(-kz[e >> 1], qs[n][e & 1], sc[n][e]) * (sk[e >> 1] * qf[n][e & 1]);
-        if (!plain) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int hf = e >> 1, c = e & 1;
-              float x = sc[n][e];
-              if (P.cap > 0.f) x = P.cap * kLog2e * tanh_score(x);
-              const int dist = qpos[n][c] - (k.kpos + g + 8 * hf);
-              x = fmaf(-slope[n][c], static_cast<float>(dist), x);
-              const bool seen =
-                  dist >= 0 && (P.window == 0 || dist < P.window) && k.local + g + 8 * hf < k.limit;
-              sc[n][e] = seen ? x : -INFINITY;
+            for (int hf = 0; hf < 2; ++hf) {
+              sk[gr][hf] = reinterpret_cast<const float*>(x + St::SC0)[g + 8 * hf];
+              sv[gr][hf] = reinterpret_cast<const float*>(x + St::SC0)[16 + g + 8 * hf];
+              kz[gr][hf] = static_cast<float>(x[St::SC0 + 128 + g + 8 * hf]);
             }
-          // rows behind the last key hold anything
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-            if (k.local + g + 8 * hf >= k.limit) sv[hf] = 0.f;
-        }
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+              for (int e = 0; e < 4; ++e) sc[gr][n][e] = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) raise |= sc[n][e] > m[n][e & 1] + (kLift + kLazy);
-        // ---- references: rescale only when a maximum has moved far
+            for (int c = 0; c < BITS / 4; ++c) {
+              const uint4 a4 = *reinterpret_cast<const uint4*>(x + St::k_at(g, t + 4 * c));
+              const uint4 b4 = *reinterpret_cast<const uint4*>(x + St::k_at(g + 8, t + 4 * c));
+              const uint32_t wa[4] = {a4.x, a4.y, a4.z, a4.w}, wb[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {   // infinities and NaN set none
-          const float a = fabsf(sv[hf]);
-          svmax = fmaxf(svmax, a <= 3.0e38f ? a : 0.f);
-        }
-        raise |= svmax > svr;
-        if (__any_sync(0xffffffffu, raise)) {
+              for (int w = 0; w < 4; ++w) {
+                if (BITS == 4) {
+                  const uint32_t a8 = wa[w] >> 8, b8 = wb[w] >> 8;
+                  const uint32_t f0[4] = {wa[w] & 0x000F000Fu, wb[w] & 0x000F000Fu,
+                                          wa[w] & 0x00F000F0u, wb[w] & 0x00F000F0u};
+                  const uint32_t f1[4] = {a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u,
+                                          b8 & 0x00F000F0u};
 #pragma unroll
-          for (int of = 4; of < 32; of <<= 1)
-            svmax = fmaxf(svmax, __shfl_xor_sync(0xffffffffu, svmax, of));
-          // a power of two at or above svmax, between 2^-126 and 2^126
-          const int e2 = max(1, min(253, static_cast<int>(__float_as_uint(svmax) >> 23) + 1));
-          const float nsv = fmaxf(svr, __uint_as_float(static_cast<uint32_t>(e2) << 23));
-          const float down = svr > 0.f ? svr / nsv : 0.f;
-          svr = nsv;
-          svi = 1.0f / nsv;
+                  for (int n = 0; n < NT; ++n) {
+                    mma16816(sc[gr][n], f0, qb[n][2 * w][0], qb[n][2 * w][1]);
+                    mma16816(sc[gr][n], f1, qb[n][2 * w + 1][0], qb[n][2 * w + 1][1]);
+                  }
+                } else {
+                  const uint32_t f0[4] = {__byte_perm(wa[w], 0u, 0x4140u), __byte_perm(wb[w], 0u, 0x4140u),
+                                          __byte_perm(wa[w], 0u, 0x4342u), __byte_perm(wb[w], 0u, 0x4342u)};
+#pragma unroll
+                  for (int n = 0; n < NT; ++n)
+                    mma16816(sc[gr][n], f0, qb[n][4 * c + w][0], qb[n][4 * c + w][1]);
+                }
+              }
+            }
+          }
+          // ---- scores; without a cap or slopes the row's factor waits for the exponential
+          const bool plain = !special && have == 3u && local + 32 <= limit && kpos + 31 <= qmin &&
+                             (P.window == 0 || qmax - kpos < P.window);
+#pragma unroll
+          for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                sc[gr][n][e] = fmaf(-kz[gr][e >> 1], qs[n][e & 1], sc[gr][n][e]) * sk[gr][e >> 1];
+          if (!plain) {
+#pragma unroll
+            for (int gr = 0; gr < 2; ++gr) {
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int hf = e >> 1, c = e & 1;
+                  float x = sc[gr][n][e];
+                  const int dist = qpos[n][c] - (kpos + 16 * gr + g + 8 * hf);
+                  if (special) {
+                    x *= qf[n][c];
+                    if (P.cap > 0.f) x = P.cap * kLog2e * tanh_score(x);
+                    x = fmaf(-slope[n][c], static_cast<float>(dist), x);
+                  }
+                  const bool seen = dist >= 0 && (P.window == 0 || dist < P.window) &&
+                                    local + 16 * gr + g + 8 * hf < limit && ((have >> gr) & 1u);
+                  sc[gr][n][e] = seen ? x : -INFINITY;
+                }
+              // rows behind the last key, and a group that is not there, hold anything
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+                if (local + 16 * gr + g + 8 * hf >= limit || !((have >> gr) & 1u)) sv[gr][hf] = 0.f;
+            }
+          }
+          // ---- references: rescale only when a maximum has moved far
+          float mx[NT][2];
+          bool raise = false;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float mx = fmaxf(fmaxf(sc[n][c], sc[n][2 + c]) - kLift, m[n][c]);
+              mx[n][c] = fmaxf(fmaxf(sc[0][n][c], sc[0][n][2 + c]), fmaxf(sc[1][n][c], sc[1][n][2 + c])) *
+                         ff[n][c];
+              raise |= mx[n][c] > m[n][c] + (kLift + kLazy);
+            }
+          const float sva = fmaxf(fmaxf(fabsf(sv[0][0]), fabsf(sv[0][1])), fmaxf(fabsf(sv[1][0]), fabsf(sv[1][1])));
+          raise |= sva > svr;
+          if (__any_sync(0xffffffffu, raise)) {
+            float svmax = 0.f;             // infinities and NaN set none
 #pragma unroll
-              for (int of = 4; of < 32; of <<= 1)
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, of));
-              const float f = m[n][c] == -INFINITY ? 0.f : ex2(m[n][c] - mx);
-              m[n][c] = mx;
-              l[n][c] *= f;
+            for (int j = 0; j < 4; ++j) {
+              const float a = fabsf(sv[j >> 1][j & 1]);
+              svmax = fmaxf(svmax, a <= 3.0e38f ? a : 0.f);
+            }
 #pragma unroll
-              for (int i8 = 0; i8 < 8; ++i8) {
-                o[n][i8][c] *= f * down;
-                o[n][i8][2 + c] *= f * down;
+            for (int of = 4; of < 32; of <<= 1)
+              svmax = fmaxf(svmax, __shfl_xor_sync(0xffffffffu, svmax, of));
+            // a power of two at or above svmax, between 2^-126 and 2^126
+            const int e2 = max(1, min(253, static_cast<int>(__float_as_uint(svmax) >> 23) + 1));
+            const float nsv = fmaxf(svr, __uint_as_float(static_cast<uint32_t>(e2) << 23));
+            const float down = svr > 0.f ? svr / nsv : 0.f;
+            svr = nsv;
+            svi = 1.0f / nsv;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float top = fmaxf(mx[n][c] - kLift, m[n][c]);
+#pragma unroll
+                for (int of = 4; of < 32; of <<= 1)
+                  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, of));
+                const float f = m[n][c] == -INFINITY ? 0.f : ex2(m[n][c] - top);
+                m[n][c] = top;
+                l[n][c] *= f;
+#pragma unroll
+                for (int i8 = 0; i8 < 8; ++i8) {
+                  o[n][i8][c] *= f * down;
+                  o[n][i8][2 + c] *= f * down;
+                }
               }
-            }
-        }
-        // ---- weights, as fp16 pairs (high, low), to the B operand's layout
-        uint32_t ph[NT][2], pl[NT][2];
-        const float wv[2] = {sv[0] * svi, sv[1] * svi};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float p[4], w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = ex2(sc[n][e] - m[n][e & 1]);
-            w[e] = p[e] * wv[e >> 1];
-          }
-          if (!plain) {                    // no reference yet, or a hidden key's infinite scale
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (sc[n][e] == -INFINITY) p[e] = 0.f;
-              if (p[e] == 0.f) w[e] = 0.f;
-            }
           }
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const float w0 = w[2 * hf], w1 = w[2 * hf + 1];
-            l[n][0] += p[2 * hf];
-            l[n][1] += p[2 * hf + 1];
-            const __half2 hi = __floats2half2_rn(w0, w1);
-            const float2 back = __half22float2(hi);
-            const uint32_t lo = h2_bits(__floats2half2_rn(w0 - back.x, w1 - back.y));
-            if (PAIR) {
-              ph[n][hf] = transpose8x8(t < 2 ? h2_bits(hi) : lo);
-            } else {
-              ph[n][hf] = transpose8x8(h2_bits(hi));
-              pl[n][hf] = transpose8x8(lo);
-            }
-          }
-        }
-        // ---- O^T += C_v^T w: dims 16 g + 2 i + {0, 1} in m-tile i
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t va[8], vb[8];           // 8 dims of key pairs (2t, 2t+1) and (2t+8, 2t+9)
-#pragma unroll
-          for (int pr = 0; pr < 2; ++pr) {
-            uint32_t(&dst)[8] = pr ? vb : va;
-            if (BITS == 4) {
-              const int at = 8 * (g & 1) + 4 * half;
-              const uint32_t vz16 = ((vz[pr] & 0x000F000Fu) << 4) | 0x80008000u;
-              const uint32_t a = *reinterpret_cast<const uint32_t*>(
-                  sl + St::V0 + St::v_at(2 * t + 8 * pr, g >> 1) + at);
-              const uint32_t bb = *reinterpret_cast<const uint32_t*>(
-                  sl + St::V0 + St::v_at(2 * t + 1 + 8 * pr, g >> 1) + at);
-#pragma unroll
-              for (int hw = 0; hw < 2; ++hw) {
-                const uint32_t mix = __byte_perm(a, bb, hw ? 0x7632u : 0x5410u), m8 = mix >> 8;
-                dst[4 * hw] = add_bits(mix & 0x000F000Fu, vz[pr]);
-                dst[4 * hw + 1] = add_bits(mix & 0x00F000F0u, vz16);
-                dst[4 * hw + 2] = add_bits(m8 & 0x000F000Fu, vz[pr]);
-                dst[4 * hw + 3] = add_bits(m8 & 0x00F000F0u, vz16);
-              }
-            } else {
-              const uint2 a2 = *reinterpret_cast<const uint2*>(
-                  sl + St::V0 + St::v_at(2 * t + 8 * pr, g) + 8 * half);
-              const uint2 b2 = *reinterpret_cast<const uint2*>(
-                  sl + St::V0 + St::v_at(2 * t + 1 + 8 * pr, g) + 8 * half);
-#pragma unroll
-              for (int hw = 0; hw < 2; ++hw) {
-                const uint32_t a = hw ? a2.y : a2.x, bb = hw ? b2.y : b2.x;
-                const uint32_t lo = __byte_perm(a, bb, 0x5140u), hi = __byte_perm(a, bb, 0x7362u);
-                dst[4 * hw] = add_bits(__byte_perm(lo, 0u, 0x4140u), vz[pr]);
-                dst[4 * hw + 1] = add_bits(__byte_perm(lo, 0u, 0x4342u), vz[pr]);
-                dst[4 * hw + 2] = add_bits(__byte_perm(hi, 0u, 0x4140u), vz[pr]);
-                dst[4 * hw + 3] = add_bits(__byte_perm(hi, 0u, 0x4342u), vz[pr]);
-              }
-            }
-          }
-#pragma unroll
-          for (int i4 = 0; i4 < 4; ++i4) {
-            const uint32_t a[4] = {va[2 * i4], va[2 * i4 + 1], vb[2 * i4], vb[2 * i4 + 1]};
+          for (int gr = 0; gr < 2; ++gr) {
+            // ---- weights, as fp16 pairs (high, low), to the B operand's layout
+            uint32_t ph[NT][2], pl[NT][2];
+            const float wv[2] = {sv[gr][0] * svi, sv[gr][1] * svi};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              mma16816(o[n][4 * half + i4], a, ph[n][0], ph[n][1]);
-              if (!PAIR) mma16816(o[n][4 * half + i4], a, pl[n][0], pl[n][1]);
+              float p[4], w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                p[e] = ex2(fmaf(sc[gr][n][e], ff[n][e & 1], -m[n][e & 1]));
+                w[e] = p[e] * wv[e >> 1];
+              }
+              if (!plain) {                // no reference yet, or a hidden key's infinite scale
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if (sc[gr][n][e] == -INFINITY) p[e] = 0.f;
+                  if (p[e] == 0.f) w[e] = 0.f;
+                }
+              }
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                const float w0 = w[2 * hf], w1 = w[2 * hf + 1];
+                l[n][0] += p[2 * hf];
+                l[n][1] += p[2 * hf + 1];
+                const __half2 hi = __floats2half2_rn(w0, w1);
+                const float2 back = __half22float2(hi);
+                const uint32_t lo = h2_bits(__floats2half2_rn(w0 - back.x, w1 - back.y));
+                if (PAIR) {
+                  ph[n][hf] = transpose8x8(t < 2 ? h2_bits(hi) : lo);
+                } else {
+                  ph[n][hf] = transpose8x8(h2_bits(hi));
+                  pl[n][hf] = transpose8x8(lo);
+                }
+              }
+            }
+            // ---- O^T += (C_v - z_v)^T w: dims 16 g + 2 i + {0, 1} in m-tile i
+            const uint8_t* x = sl + gr * St::GROUP;
+            uint32_t vz[2];                // zero points of keys 2t, 2t + 1 (+ 8): fp16 -z 2^-24
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+              vz[hf] = __byte_perm(reinterpret_cast<const uint16_t*>(x + St::SC0 + 144)[t + 4 * hf], 0u, 0x4140u) |
+                       0x80008000u;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t va[8], vb[8];       // 8 dims of key pairs (2t, 2t+1) and (2t+8, 2t+9)
+#pragma unroll
+              for (int pr = 0; pr < 2; ++pr) {
+                uint32_t(&dst)[8] = pr ? vb : va;
+                if (BITS == 4) {
+                  const int at = 8 * (g & 1) + 4 * half;
+                  const uint32_t vz16 = ((vz[pr] & 0x000F000Fu) << 4) | 0x80008000u;
+                  const uint32_t a = *reinterpret_cast<const uint32_t*>(
+                      x + St::V0 + St::v_at(2 * t + 8 * pr, g >> 1) + at);
+                  const uint32_t bb = *reinterpret_cast<const uint32_t*>(
+                      x + St::V0 + St::v_at(2 * t + 1 + 8 * pr, g >> 1) + at);
+#pragma unroll
+                  for (int hw = 0; hw < 2; ++hw) {
+                    const uint32_t mix = __byte_perm(a, bb, hw ? 0x7632u : 0x5410u), m8 = mix >> 8;
+                    dst[4 * hw] = add_bits(mix & 0x000F000Fu, vz[pr]);
+                    dst[4 * hw + 1] = add_bits(mix & 0x00F000F0u, vz16);
+                    dst[4 * hw + 2] = add_bits(m8 & 0x000F000Fu, vz[pr]);
+                    dst[4 * hw + 3] = add_bits(m8 & 0x00F000F0u, vz16);
+                  }
+                } else {
+                  const uint2 a2 = *reinterpret_cast<const uint2*>(
+                      x + St::V0 + St::v_at(2 * t + 8 * pr, g) + 8 * half);
+                  const uint2 b2 = *reinterpret_cast<const uint2*>(
+                      x + St::V0 + St::v_at(2 * t + 1 + 8 * pr, g) + 8 * half);
+#pragma unroll
+                  for (int hw = 0; hw < 2; ++hw) {
+                    const uint32_t a = hw ? a2.y : a2.x, bb = hw ? b2.y : b2.x;
+                    const uint32_t lo = __byte_perm(a, bb, 0x5140u), hi = __byte_perm(a, bb, 0x7362u);
+                    dst[4 * hw] = add_bits(__byte_perm(lo, 0u, 0x4140u), vz[pr]);
+                    dst[4 * hw + 1] = add_bits(__byte_perm(lo, 0u, 0x4342u), vz[pr]);
+                    dst[4 * hw + 2] = add_bits(__byte_perm(hi, 0u, 0x4140u), vz[pr]);
+                    dst[4 * hw + 3] = add_bits(__byte_perm(hi, 0u, 0x4342u), vz[pr]);
+                  }
+                }
+              }
+#pragma unroll
+              for (int i4 = 0; i4 < 4; ++i4) {
+                const uint32_t a[4] = {va[2 * i4], va[2 * i4 + 1], vb[2 * i4], vb[2 * i4 + 1]};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  mma16816(o[n][4 * half + i4], a, ph[n][0], ph[n][1]);
+                  if (!PAIR) mma16816(o[n][4 * half + i4], a, pl[n][0], pl[n][1]);
+                }
+              }
             }
           }
+          __syncwarp();
         }
-        __syncwarp();
+        fetch(local + 2 * TILE, pg, slot);
+        pages_of(local + 3 * TILE, pg);
       }
-      fetch(i + DEPTH, page_next, slot);
-      page_next = page_of(i + DEPTH + 1);
+      cp_async_wait<0>();
+      __syncwarp();
     }
-    cp_async_wait<0>();
 
     // ---- the warps' results into shared memory, at a common maximum
 #pragma unroll
@@ -584,7 +616,7 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
           }
           x = x * 16777216.0f * svr;
           y = y * (BITS == 4 ? 1048576.0f : 16777216.0f) * svr;
-          if (r < R) *reinterpret_cast<float2*>(&sm_o[warp][r][16 * g + 2 * i]) = make_float2(x, y);
+          if (r < R) *reinterpret_cast<float2*>(&sm_o(warp)[r][16 * g + 2 * i]) = make_float2(x, y);
         }
       }
     __syncthreads();
@@ -602,7 +634,7 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) {
         const float f = sm_m[w][r] == -INFINITY ? 0.f : ex2(sm_m[w][r] - M);
-        if (f != 0.f) acc[r] = fmaf(f, sm_o[w][r][tid], acc[r]);
+        if (f != 0.f) acc[r] = fmaf(f, sm_o(w)[r][tid], acc[r]);
         ll[r] = fmaf(f, sm_l[w][r], ll[r]);
       }
     }

@@ -14,7 +14,7 @@ namespace paged {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int TILE = 64;                   // keys per CTA step of the streaming kernel
+constexpr int TILE = 128;                  // keys per CTA step of the streaming kernel
 
 struct AttnParams {
   const __nv_bfloat16* q;

@@ -8,10 +8,15 @@
 // but the norm's factor, which is one number per vector, so
 //     y = f * H (R (w * x)),  f = rsqrt(mean x^2 + eps) / sqrt(128)
 // with R the rotary map: the factor is applied once, after the butterflies.
-// A rotary partner in the half layout sits rot / 2 channels away; its chunk is
-// read again (an L1 hit) rather than exchanged between lanes, which serves
-// every rot that is a multiple of 16 and both layouts with one data layout.
+// The usual rotary map (half layout, whole head) pairs a lane's two chunks, so
+// its cosines and sines stay in registers for all of a token's heads; for the
+// others (interleaved, or part of the head, any multiple of 16) the partner's
+// chunk is read again (an L1 hit) rather than exchanged between lanes.
 // H128's bits 0-2 and 6 run inside the lane, bits 3-5 across the 8 lanes.
+//
+// A warp takes a token (or, for few tokens, a part of its heads): it finds the
+// token's place once, while the first heads' values are already on their way,
+// and always has the next heads' loads in flight.
 //
 // Q is computed in float32 (its output is bf16).  K is computed in double
 // precision and rounded once to float32, so its codes are those of the exact
@@ -41,16 +46,20 @@ struct AppendParams {
   float eps;
   __nv_bfloat16* q_out;
   int hq, jq, jk;                          // query heads; warp jobs per token of Q and of K
+  int split;                               // warps per token
 };
 
-__device__ __forceinline__ void chunk8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
   const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     x[2 * e] = __uint_as_float(ws[e] << 16);
     x[2 * e + 1] = __uint_as_float(ws[e] & 0xFFFF0000u);
   }
+}
+
+__device__ __forceinline__ void chunk8(const __nv_bfloat16* p, float (&x)[8]) {
+  unpack8(*reinterpret_cast<const uint4*>(p), x);
 }
 
 __device__ __forceinline__ void floats8(const float* p, float (&x)[8]) {
@@ -60,84 +69,146 @@ __device__ __forceinline__ void floats8(const float* p, float (&x)[8]) {
   x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
-// y = f * H (R (w * x)) of one vector over its 8 lanes, in R's precision.
+// The rotary factors of a token that a lane keeps (half layout, whole head:
+// pairs 8 s .. 8 s + 7, channel 8 s + e with 64 + 8 s + e).
+struct Factors {
+  float c[8], s[8];
+};
+
+// y = H128's bits 3-5, across the 8 lanes of a vector.
 template <class R>
-__device__ __forceinline__ void head_forward(const __nv_bfloat16* src, const float* w,
-                                             const float* cs, const float* sn, int rot,
-                                             bool interleaved, float eps, int s, unsigned mask,
-                                             R (&y)[16]) {
-  R sum = 0;
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int e0 = 64 * c + 8 * s;
-    float x[8], g[8];
-    chunk8(src + e0, x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[8 * c + e] = x[e];
-    if (w) {
-      floats8(w + e0, g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sum += static_cast<R>(x[e]) * static_cast<R>(x[e]);
-        y[8 * c + e] *= static_cast<R>(g[e]);
-      }
-    }
-    if (e0 < rot) {
-      if (interleaved) {
-        const float4 c4 = __ldg(reinterpret_cast<const float4*>(cs + e0 / 2));
-        const float4 s4 = __ldg(reinterpret_cast<const float4*>(sn + e0 / 2));
-        const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const R a = y[8 * c + 2 * e], b = y[8 * c + 2 * e + 1];
-          const R C = cc[e], S = ss[e];
-          y[8 * c + 2 * e] = a * C - b * S;
-          y[8 * c + 2 * e + 1] = b * C + a * S;
-        }
-      } else {
-        const int half = rot >> 1;
-        const bool upper = e0 >= half;
-        const int p0 = upper ? e0 - half : e0 + half, i0 = upper ? p0 : e0;
-        float b[8], cc[8], ss[8];
-        chunk8(src + p0, b);
-        floats8(cs + i0, cc);
-        floats8(sn + i0, ss);
-        if (w) floats8(w + p0, g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          R t = b[e];
-          if (w) t *= static_cast<R>(g[e]);
-          t *= static_cast<R>(ss[e]);
-          y[8 * c + e] = y[8 * c + e] * static_cast<R>(cc[e]) + (upper ? t : -t);
-        }
-      }
-    }
-  }
-  R f = static_cast<R>(0.088388347648318440550);   // 1/sqrt(128)
-  if (w) {
-#pragma unroll
-    for (int o = 1; o < LPV; o <<= 1) sum += __shfl_xor_sync(mask, sum, o);
-    f *= R(1) / sqrt(sum * R(1.0 / D) + static_cast<R>(eps));
-  }
-#pragma unroll
-  for (int h = 1; h < 16; h <<= 1) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      if ((e & h) == 0) {
-        const R a = y[e], b = y[e + h];
-        y[e] = a + b;
-        y[e + h] = a - b;
-      }
-    }
-  }
+__device__ __forceinline__ void across(R (&y)[16], int s, unsigned mask) {
 #pragma unroll
   for (int o = 1; o < LPV; o <<= 1) {
     const R sg = (s & o) ? R(-1) : R(1);
 #pragma unroll
     for (int e = 0; e < 16; ++e) y[e] = fma(sg, y[e], __shfl_xor_sync(mask, y[e], o));
   }
+}
+
+// R (w * x) of one vector over its 8 lanes, in R's precision, and the norm's
+// sum of squares of this lane's values.  raw: chunks s and s + 8.
+template <class R, bool WHOLE>
+__device__ __forceinline__ R scale_and_turn(const uint4 (&raw)[2], const __nv_bfloat16* src, const float* w,
+                                            const Factors& fac, const float* cs, const float* sn,
+                                            int rot, bool interleaved, int s, R (&y)[16]) {
+  R sum = 0;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    float x[8], g[8];
+    unpack8(raw[c], x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[8 * c + e] = x[e];
+    if (w) {
+      floats8(w + 64 * c + 8 * s, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sum += static_cast<R>(x[e]) * static_cast<R>(x[e]);
+        y[8 * c + e] *= static_cast<R>(g[e]);
+      }
+    }
+  }
+  if (WHOLE) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const R a = y[e], b = y[8 + e], C = fac.c[e], S = fac.s[e];
+      y[e] = a * C - b * S;
+      y[8 + e] = b * C + a * S;
+    }
+    return sum;
+  }
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int e0 = 64 * c + 8 * s;
+    if (e0 >= rot) continue;
+    if (interleaved) {
+      const float4 c4 = __ldg(reinterpret_cast<const float4*>(cs + e0 / 2));
+      const float4 s4 = __ldg(reinterpret_cast<const float4*>(sn + e0 / 2));
+      const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const R a = y[8 * c + 2 * e], b = y[8 * c + 2 * e + 1];
+        const R C = cc[e], S = ss[e];
+        y[8 * c + 2 * e] = a * C - b * S;
+        y[8 * c + 2 * e + 1] = b * C + a * S;
+      }
+    } else {
+      const int half = rot >> 1;
+      const bool upper = e0 >= half;
+      const int p0 = upper ? e0 - half : e0 + half, i0 = upper ? p0 : e0;
+      float b[8], cc[8], ss[8], g[8];
+      chunk8(src + p0, b);
+      floats8(cs + i0, cc);
+      floats8(sn + i0, ss);
+      if (w) floats8(w + p0, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        R t = b[e];
+        if (w) t *= static_cast<R>(g[e]);
+        t *= static_cast<R>(ss[e]);
+        y[8 * c + e] = y[8 * c + e] * static_cast<R>(cc[e]) + (upper ? t : -t);
+      }
+    }
+  }
+  return sum;
+}
+
+// f H, f = rsqrt(mean x^2 + eps) / sqrt(128) (w) or 1 / sqrt(128): in double.
+__device__ __forceinline__ void finish(double (&y)[16], double sum, bool norm, float eps, int s, unsigned mask) {
+  double f = 0.088388347648318440550;      // 1/sqrt(128)
+  if (norm) {
+#pragma unroll
+    for (int o = 1; o < LPV; o <<= 1) sum += __shfl_xor_sync(mask, sum, o);
+    f *= 1.0 / sqrt(sum * (1.0 / D) + static_cast<double>(eps));
+  }
+#pragma unroll
+  for (int h = 1; h < 16; h <<= 1) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      if ((e & h) == 0) {
+        const double a = y[e], b = y[e + h];
+        y[e] = a + b;
+        y[e + h] = a - b;
+      }
+    }
+  }
+  across(y, s, mask);
 #pragma unroll
   for (int e = 0; e < 16; ++e) y[e] *= f;
+}
+
+// The same in float32, two values (the lane's two chunks) an instruction.
+__device__ __forceinline__ void finish(float (&y)[16], float sum, bool norm, float eps, int s, unsigned mask) {
+  float f = 0.088388347648318440550f;
+  if (norm) {
+#pragma unroll
+    for (int o = 1; o < LPV; o <<= 1) sum += __shfl_xor_sync(mask, sum, o);
+    f *= 1.0f / sqrtf(sum * (1.0f / D) + eps);
+  }
+  f2 v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = f2{(y[e] + y[8 + e]) * f, (y[e] - y[8 + e]) * f};
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if ((e & h) == 0) {
+        const f2 a = v[e], b = v[e + h];
+        v[e] = add2(a, b);
+        v[e + h] = sub2(a, b);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < LPV; o <<= 1) {
+    const float sg = (s & o) ? -1.f : 1.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = fma2(f2{sg, sg}, v[e],
+                  f2{__shfl_xor_sync(mask, v[e].x, o), __shfl_xor_sync(mask, v[e].y, o)});
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = v[e].x, y[8 + e] = v[e].y;
 }
 
 // Quantizes one vector held by 8 lanes (lane s: chunks s and s + 8) into row
@@ -178,101 +249,132 @@ __device__ __forceinline__ void store_quantized(const float (&y)[16], int s, uns
   }
 }
 
-template <int BITS>
-__global__ void __launch_bounds__(256) append_kernel(AppendParams P) {
+// WHOLE: half layout over the whole head.
+template <int BITS, bool WHOLE>
+__global__ void __launch_bounds__(256) append_kernel(const AppendParams P) {
   const int lane = threadIdx.x & 31, s = lane & (LPV - 1), vec = lane / LPV;
   const unsigned mask = 0xFFu << (lane & 24);
-  const int jobs = P.jq + 2 * P.jk;
-  const int64_t n = P.batch.T * jobs;
+  const int jobs = P.jq + 2 * P.jk;        // four heads each: Q, K, V
+  const int64_t items = P.batch.T * P.split;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-  for (int64_t j = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); j < n;
-       j += step) {
-    const int64_t t = j / jobs;
-    int job = static_cast<int>(j - t * jobs);
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items;
+       it += step) {
+    const int64_t t = P.split == 1 ? it : it / P.split;
+    const int part = static_cast<int>(it - t * P.split);
+    // this lane's head of a job, the last one where there are no four (what it gives is not stored)
+    auto source = [&](int job) {
+      if (job < P.jq) return P.q + t * P.sq + min(job * VPW + vec, P.hq - 1) * D;
+      job -= P.jq;
+      const bool is_v = job >= P.jk;
+      const int head = min((is_v ? job - P.jk : job) * VPW + vec, P.pages.hkv - 1);
+      return is_v ? P.v + t * P.sv + head * D : P.k + t * P.sk + head * D;
+    };
+    const __nv_bfloat16* src = source(part);
+    uint4 raw[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) raw[c] = *reinterpret_cast<const uint4*>(src + 64 * c + 8 * s);
     int pos, page;
     bool bad;
     bool ok = locate(P.pages, P.batch, t, pos, page, bad);
     if (ok && P.cos && pos >= P.max_pos) bad = true, ok = false;
     if (!ok) {
-      if (bad && lane == 0 && job == 0) record_status(SQ_ERR_INVALID_ARG);
+      if (bad && lane == 0 && part == 0) record_status(SQ_ERR_INVALID_ARG);
       continue;
     }
     const float* cs = P.cos + static_cast<int64_t>(pos) * (P.rot >> 1);
     const float* sn = P.sin + static_cast<int64_t>(pos) * (P.rot >> 1);
-    if (job < P.jq) {
-      const int head = job * VPW + vec;
-      if (head >= P.hq) continue;          // whole groups of 8 lanes leave
-      float y[16];
-      head_forward<float>(P.q + t * P.sq + head * D, P.q_norm, cs, sn, P.rot, P.interleaved, P.eps,
-                          s, mask, y);
-      __nv_bfloat16* dst = P.q_out + (t * P.hq + head) * D + 8 * s;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float* v = y + 8 * c;
-        *reinterpret_cast<uint4*>(dst + 64 * c) =
-            make_uint4(kv::bf16x2(v[0], v[1]), kv::bf16x2(v[2], v[3]), kv::bf16x2(v[4], v[5]),
-                       kv::bf16x2(v[6], v[7]));
-      }
-      continue;
+    Factors fac;
+    if (WHOLE) {
+      floats8(cs + 8 * s, fac.c);
+      floats8(sn + 8 * s, fac.s);
     }
-    job -= P.jq;
-    const bool is_v = job >= P.jk;
-    const int head = (is_v ? job - P.jk : job) * VPW + vec;
-    if (head >= P.pages.hkv) continue;
-    const int64_t g = group_of(P.pages, page, head, pos & ((1 << P.pages.lps) - 1));
-    float x[16];
-    if (is_v) {
-      const __nv_bfloat16* src = P.v + t * P.sv + head * D + 8 * s;
-      float a[8], b[8];
-      chunk8(src, a);
-      chunk8(src + 64, b);
+    for (int job = part; job < jobs; job += P.split) {
+      const __nv_bfloat16* now = src;
+      const uint4 mine[2] = {raw[0], raw[1]};
+      if (job + P.split < jobs) {
+        src = source(job + P.split);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = a[e], x[8 + e] = b[e];
-      store_quantized<BITS>(x, s, mask, P.pages.vc, P.pages.vs, P.pages.vz, g);
-    } else {
-      double y[16];
-      head_forward<double>(P.k + t * P.sk + head * D, P.k_norm, cs, sn, P.rot, P.interleaved, P.eps,
-                           s, mask, y);
+        for (int c = 0; c < 2; ++c) raw[c] = *reinterpret_cast<const uint4*>(src + 64 * c + 8 * s);
+      }
+      if (job < P.jq) {
+        const int head = job * VPW + vec;
+        float y[16];
+        const float sum = scale_and_turn<float, WHOLE>(mine, now, P.q_norm, fac, cs, sn, P.rot, P.interleaved, s, y);
+        finish(y, sum, P.q_norm != nullptr, P.eps, s, mask);
+        if (head < P.hq) {
+          __nv_bfloat16* dst = P.q_out + (t * P.hq + head) * D + 8 * s;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = static_cast<float>(y[e]);
-      store_quantized<BITS>(x, s, mask, P.pages.kc, P.pages.ks, P.pages.kz, g);
+          for (int c = 0; c < 2; ++c) {
+            const float* v = y + 8 * c;
+            *reinterpret_cast<uint4*>(dst + 64 * c) =
+                make_uint4(kv::bf16x2(v[0], v[1]), kv::bf16x2(v[2], v[3]), kv::bf16x2(v[4], v[5]),
+                           kv::bf16x2(v[6], v[7]));
+          }
+        }
+        continue;
+      }
+      const bool is_v = job >= P.jq + P.jk;
+      const int head = (job - P.jq - (is_v ? P.jk : 0)) * VPW + vec;
+      float x[16];
+      if (is_v) {
+        float a[8], b[8];
+        unpack8(mine[0], a);
+        unpack8(mine[1], b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = a[e], x[8 + e] = b[e];
+      } else {
+        double y[16];
+        const double sum = scale_and_turn<double, WHOLE>(mine, now, P.k_norm, fac, cs, sn, P.rot, P.interleaved, s, y);
+        finish(y, sum, P.k_norm != nullptr, P.eps, s, mask);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = static_cast<float>(y[e]);
+      }
+      if (head < P.pages.hkv) {            // whole groups of 8 lanes
+        const int64_t g = group_of(P.pages, page, head, pos & ((1 << P.pages.lps) - 1));
+        store_quantized<BITS>(x, s, mask, is_v ? P.pages.vc : P.pages.kc, is_v ? P.pages.vs : P.pages.ks,
+                              is_v ? P.pages.vz : P.pages.kz, g);
+      }
     }
   }
 }
 
 // Rows of the pages back to bf16, 16 lanes per head vector (8 codes each).
 template <int BITS>
-__global__ void __launch_bounds__(256) dequant_kernel(Pages P, Batch b, __nv_bfloat16* k_out,
-                                                      __nv_bfloat16* v_out) {
+__global__ void __launch_bounds__(256) dequant_kernel(const Pages P, const Batch b, __nv_bfloat16* k_out,
+                                                      __nv_bfloat16* v_out, int split) {
   constexpr int RB = D * BITS / 8;
   const int lane = threadIdx.x & 31, c = lane & 15;
-  const int vecs = 2 * P.hkv;              // K heads, then V heads
-  const int64_t n = b.T * P.hkv;           // warps take two vectors
+  const bool is_v = lane >= 16;            // a job: one head's K and V
+  const uint8_t* codes = is_v ? P.vc : P.kc;
+  const float* scales = is_v ? P.vs : P.ks;
+  const uint8_t* zeros = is_v ? P.vz : P.kz;
+  __nv_bfloat16* out = is_v ? v_out : k_out;
+  const int64_t items = b.T * split;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-  for (int64_t j = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); j < n;
-       j += step) {
-    const int64_t t = j / P.hkv;
-    const int vec = 2 * static_cast<int>(j - t * P.hkv) + (lane >> 4);
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items;
+       it += step) {
+    const int64_t t = split == 1 ? it : it / split;
+    const int part = static_cast<int>(it - t * split);
     int pos, page;
     bool bad;
     if (!locate(P, b, t, pos, page, bad)) {
-      if (bad && vec == 0 && c == 0) record_status(SQ_ERR_INVALID_ARG);
+      if (bad && part == 0 && lane == 0) record_status(SQ_ERR_INVALID_ARG);
       continue;
     }
-    if (vec >= vecs) continue;
-    const bool is_v = vec >= P.hkv;
-    const int head = is_v ? vec - P.hkv : vec;
-    const int64_t g = group_of(P, page, head, pos & ((1 << P.lps) - 1));
-    const uint8_t* src = (is_v ? P.vc : P.kc) + g * RB + c * BITS;
-    const float scale = (is_v ? P.vs : P.ks)[g];
-    const float zb = 8388608.0f + static_cast<float>((is_v ? P.vz : P.kz)[g]);
-    uint2 w;
-    if (BITS == 4)
-      w = make_uint2(*reinterpret_cast<const uint32_t*>(src), 0u);
-    else
-      w = *reinterpret_cast<const uint2*>(src);
-    __nv_bfloat16* dst = (is_v ? v_out : k_out) + (t * P.hkv + head) * D + 8 * c;
-    *reinterpret_cast<uint4*>(dst) = kv::widen8<BITS>(w, scale, zb);
+    const int64_t g0 = group_of(P, page, 0, pos & ((1 << P.lps) - 1));
+#pragma unroll 4
+    for (int head = part; head < P.hkv; head += split) {
+      const int64_t g = g0 + (static_cast<int64_t>(head) << P.lps);
+      const uint8_t* src = codes + g * RB + c * BITS;
+      const float scale = __ldg(scales + g);
+      const float zb = 8388608.0f + static_cast<float>(__ldg(zeros + g));
+      uint2 w;
+      if (BITS == 4)
+        w = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(src)), 0u);
+      else
+        w = __ldg(reinterpret_cast<const uint2*>(src));
+      *reinterpret_cast<uint4*>(out + (t * P.hkv + head) * D + 8 * c) = kv::widen8<BITS>(w, scale, zb);
+    }
   }
 }
 
@@ -282,6 +384,13 @@ Pages view(const sq_kv_pages& p) {
   Pages v{p.k_codes, p.k_scale, p.k_zero, p.v_codes, p.v_scale, p.v_zero, p.num_pages, 0, p.hkv};
   while ((1 << v.lps) < p.page_size) ++v.lps;
   return v;
+}
+
+// Warps per token: one while that fills the device (32 warps per SM), else as many as it takes, a
+// job each at most.
+int warps_per_token(int64_t T, int jobs) {
+  const int64_t want = (static_cast<int64_t>(host::num_sms()) * 32 + T - 1) / T;
+  return static_cast<int>(want < jobs ? want : jobs);
 }
 
 int grid_for(int64_t warps, int per_sm) {
@@ -311,8 +420,11 @@ sq_status run_append(const void* q, const void* k, const void* v, int64_t q_stri
   P.hq = hq;
   P.jq = (hq + VPW - 1) / VPW;
   P.jk = (pages.hkv + VPW - 1) / VPW;
-  auto kern = pages.bits == 8 ? append_kernel<8> : append_kernel<4>;
-  kern<<<grid_for(T * (P.jq + 2 * P.jk), 8), 256, 0, stream>>>(P);
+  P.split = warps_per_token(T, P.jq + 2 * P.jk);
+  const bool whole = cos && rot == D && !interleaved;
+  auto kern = pages.bits == 8 ? (whole ? append_kernel<8, true> : append_kernel<8, false>)
+                              : (whole ? append_kernel<4, true> : append_kernel<4, false>);
+  kern<<<grid_for(T * P.split, 8), 256, 0, stream>>>(P);
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SQ_OK : host::cuda_fail("kv_paged_append launch", e);
 }
@@ -321,9 +433,10 @@ sq_status run_dequant(const sq_kv_pages& pages, const int32_t* table, int width,
                       const int32_t* cached, int B, int64_t T, void* k_out, void* v_out,
                       cudaStream_t stream) {
   auto kern = pages.bits == 8 ? dequant_kernel<8> : dequant_kernel<4>;
-  kern<<<grid_for(T * pages.hkv, 8), 256, 0, stream>>>(
+  const int split = warps_per_token(T, pages.hkv);
+  kern<<<grid_for(T * split, 8), 256, 0, stream>>>(
       view(pages), Batch{table, cu, cached, width, B, T}, static_cast<__nv_bfloat16*>(k_out),
-      static_cast<__nv_bfloat16*>(v_out));
+      static_cast<__nv_bfloat16*>(v_out), split);
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SQ_OK : host::cuda_fail("kv_paged_dequant launch", e);
 }
