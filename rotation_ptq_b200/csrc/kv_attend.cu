@@ -840,7 +840,7 @@ AttnPlan make_plan(int64_t T, int hq, int hkv, int B, int max_q, int64_t keys, i
     p.ex_ml = take(static_cast<size_t>(p.tile_split) * T * hq * 2 * 4);
   } else if (p.tile) {
     const int64_t slots = (T * G / kTileRows + B) * hkv, tiles = (keys + prefix_len + 127) / 128;
-    int64_t s = have_ws ? 2 * sms / slots : 1;
+    int64_t s = have_ws ? sms / slots : 1;
     if (s > (tiles + 1) / 2) s = (tiles + 1) / 2;
     if (s < 1 || slots > static_cast<int64_t>(kCountBytes / 4)) s = 1;
     p.tile_split = static_cast<int>(s);

@@ -3,7 +3,7 @@
 //
 // A unit is up to 256 rows (token, query head of one KV head) in two halves of
 // 128, and a run of 128-key tiles.  Per half and tile
-//     S = Q K_int^T            (tensor memory, f32; Q and codes exact in fp16)
+//     S = Q K_int^T            (tensor memory, f32; Q and codes exact in fp16), in two steps of 64 keys
 //     y = S sk,  p = exp2(y f_row - m),  P = fp16(p sv)      (tensor memory)
 //     O += P V_int             (A from tensor memory, f32)
 // with K_int, V_int the codes less their zero points.  The row scales sk and
@@ -12,8 +12,8 @@
 //
 // Warps: 0-3 and 4-7 softmax of half 0 and 1 (a thread per row: no exchange
 // between lanes), 8-11 widen codes from global memory into swizzled shared
-// memory, 12 issues the products, 13 works out the units.  The halves alternate: while one half's
-// softmax runs, the tensor cores work for the other.
+// memory, 12 issues the products, 13 works out the units.  Each half has two buffers of 64
+// scores: the products of a step run while the softmax of the step before does.
 //
 // Two rows of work: a sequence's own rows over what it sees (splits of a
 // unit's tiles are joined by the last CTA to arrive, in order), or, for a
@@ -44,20 +44,20 @@ constexpr int OFF_SV = OFF_SK + 4 * KT * 4;
 constexpr int OFF_HID = OFF_SV + 4 * KT * 4;   // uint32 [4][8]: 4 words of hidden keys, 4 of flags
 constexpr int OFF_SVM = OFF_HID + 128;         // float [4][4]: largest value scale of 32 keys
 constexpr int OFF_BARS = OFF_SVM + 64;
-constexpr int OFF_UNITS = OFF_BARS + 256;      // TileUnit [UNITS]
+constexpr int OFF_UNITS = OFF_BARS + 512;      // TileUnit [UNITS]
 constexpr int TILE_SMEM = OFF_UNITS + UNITS * 128 + 1024;
-constexpr uint32_t TILE_TMEM = 512;        // S0, S1, O0, O1
-constexpr uint32_t IDESC_S = idesc_f16(128, 128, false, false);
+constexpr uint32_t TILE_TMEM = 512;        // S [half][buffer] of 64 columns, O [half] of 128
+constexpr uint32_t IDESC_S = idesc_f16(128, KT / 2, false, false);
 constexpr uint32_t IDESC_O = idesc_f16(128, 128, false, true);
 
 struct TileBars {
   uint64_t k_full[2], v_full[2], k_free[2], v_free[2], sc_full[4];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2];        // s, p, o: [half][buffer]
   uint64_t parts, joined, drain;           // partial results written; who joins them is known
   uint64_t u_full[UNITS], u_free[UNITS];
   uint32_t tmem, last;
 };
-static_assert(sizeof(TileBars) <= 256, "barriers");
+static_assert(sizeof(TileBars) <= 512, "barriers");
 
 __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                            uint32_t acc) {
@@ -87,6 +87,7 @@ struct TileUnit {
   const int32_t* table;                    // own pages
   int pt0, pn, ot0;                        // prefix tiles from pt0, pn of them, then own from ot0
   int first, n;                            // this CTA's tiles of the unit's list
+  int steps;                               // of 64 keys: 2 n, or one less where the last sees nothing
   int pieces, piece;                       // how many CTAs share the unit; which one this is
   int slot;                                // the unit's place among the units
 };
@@ -117,6 +118,8 @@ __device__ __forceinline__ bool tile_unit(const AttnParams& P, int64_t x, TileUn
     const int per = (u.pn + P.nsplit - 1) / P.nsplit;
     u.first = min(u.pn, u.piece * per);
     u.n = min(per, u.pn - u.first);
+    u.steps = 2 * u.n;
+    if (u.n > 0 && u.first + u.n == u.pn && ((P.prefix_len - 1) & (KT - 1)) < KT / 2) --u.steps;
     u.pieces = P.nsplit;
     return true;
   }
@@ -162,6 +165,10 @@ __device__ __forceinline__ bool tile_unit(const AttnParams& P, int64_t x, TileUn
   if (u.piece >= u.pieces) return false;
   u.first = u.piece * per;
   u.n = min(per, total - u.first);
+  u.steps = 2 * u.n;
+  if (u.n > 0 && u.first + u.n == total &&
+      ((total > u.pn ? own_high : pre) - 1) % KT < KT / 2)
+    --u.steps;
   return true;
 }
 
@@ -280,9 +287,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
       mbar_init(&bar.k_free[i], 1);
       mbar_init(&bar.v_free[i], 1);
       mbar_init(&bar.q_full[i], 4);
-      mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 4);
-      mbar_init(&bar.o_full[i], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bar.s_full[i][b], 1);
+        mbar_init(&bar.p_full[i][b], 4);
+        mbar_init(&bar.o_full[i][b], 1);
+      }
     }
     for (int i = 0; i < 4; ++i) mbar_init(&bar.sc_full[i], 4);
     mbar_init(&bar.parts, 8);
@@ -305,22 +314,21 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
   TileUnit* ring_u = reinterpret_cast<TileUnit*>(smem + OFF_UNITS);
   bool ok = true;
 
-  // registers, of the 512 x 128 that the block is launched with: 2 x 176 + 88 + 72 (4 bits) or 2 x 168 +
-  // 104 + 72 (8 bits) times 128
+  // registers, of the 512 x 128 that the block is launched with: 128 x (2 x 152 + 104 + 104)
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(BITS == 4 ? 176 : 168));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(152));
     const int hf = warp >> 2, quarter = warp & 3;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-    const uint32_t t_s = lane_base + hf * 128, t_o = lane_base + 256 + hf * 128;
+    const uint32_t t_s0 = lane_base + hf * 128, t_o = lane_base + 256 + hf * 128;
     const int r = 32 * quarter + lane;     // row within the half
-    int tiles = 0, mine = 0, splits = 0;   // tiles seen by the CTA and by this half; joins
+    int tiles = 0, mine = 0, splits = 0;   // tiles seen by the CTA, steps of this half; joins
     const bool special = P.cap > 0.f || P.slopes != nullptr;
     for (int k = 0; ok; ++k) {
       ok = __all_sync(0xffffffffu, mbar_wait(&bar.u_full[k % UNITS], (k / UNITS) & 1, spin));
       if (!ok) break;
       const volatile TileUnit& u = ring_u[k % UNITS];
-      const int rows = u.rows, n = u.n;
+      const int rows = u.rows, n = u.n, steps = u.steps;
       if (rows == 0) break;
       const bool active = hf * HALF < rows;
       const int row = hf * HALF + r;
@@ -386,92 +394,82 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
         if (lane == 0) mbar_arrive(&bar.q_full[hf]);
         const float ff = special ? 1.0f : f;
 
-        for (int i = 0; i < n && ok; ++i, ++mine) {
-          const int ring = (tiles + i) & 3;
+        for (int j = 0; j < steps; ++j, ++mine) {
+          const int tile = tiles + (j >> 1), ring = tile & 3, key0 = (j & 1) * (KT / 2), buf = mine & 1;
           // scores first: they tell that every producer warp has come past the ring's last round, so
           // that a half which skipped units cannot take an older phase of the same parity for this one
-          ok = mbar_wait(&bar.s_full[hf], mine & 1, spin);
-          ok = ok && mbar_wait(&bar.sc_full[ring], ((tiles + i) >> 2) & 1, spin);
+          ok = mbar_wait(&bar.s_full[hf][buf], (mine >> 1) & 1, spin);
+          if (ok && key0 == 0) ok = mbar_wait(&bar.sc_full[ring], (tile >> 2) & 1, spin);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          const float4* sk4 = reinterpret_cast<const float4*>(s_sk + ring * KT);
-          const float4* sv4 = reinterpret_cast<const float4*>(s_sv + ring * KT);
-          const int rel = qpos - tile_pos(P, u, i);        // distance to the tile's first key
+          const uint32_t t_s = t_s0 + buf * (KT / 2);
+          const float4* sk4 = reinterpret_cast<const float4*>(s_sk + ring * KT + key0);
+          const float4* sv4 = reinterpret_cast<const float4*>(s_sv + ring * KT + key0);
+          const int rel = qpos - tile_pos(P, u, j >> 1) - key0;          // distance to the step's first key
           if (special) {
             // capped or sloped scores, in log2 units, back to tensor memory
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < 4; ++c) {
               uint32_t v[16];
               tmem_ld16(t_s + 16 * c, v);
               tmem_ld_wait();
               const float d0 = static_cast<float>(rel - 16 * c);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float y = __uint_as_float(v[e]) * s_sk[ring * KT + 16 * c + e] * f;
-                if (P.cap > 0.f) y = P.cap * kLog2e * tanh_score(y);
-                v[e] = __float_as_uint(fmaf(-slope, d0 - static_cast<float>(e), y));
+              for (int e = 0; e < 4; ++e) {
+                const float4 s = sk4[4 * c + e];
+                const float sk[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                  float y = __uint_as_float(v[4 * e + d]) * sk[d] * f;
+                  if (P.cap > 0.f) y = P.cap * kLog2e * tanh_score(y);
+                  v[4 * e + d] = __float_as_uint(fmaf(-slope, d0 - static_cast<float>(4 * e + d), y));
+                }
               }
               tmem_st16(t_s + 16 * c, v);
             }
             tmem_st_wait();
           }
-          // keys lo .. hi - 1 of the tile are visible to this row by position
+          // ---- 64 scores (times the key's scale; the row's factor follows), hidden ones -inf; the
+          // common case is compiled by itself: branches inside cost it half its rate
+          uint32_t v[2][32];
+          tmem_ld32(t_s, v[0]);
+          tmem_ld32(t_s + 32, v[1]);
+          // keys lo .. hi - 1 of the step are visible to this row by position
           const int hi = rel + 1, lo = P.window > 0 ? hi - P.window : 0;
           const uint32_t flags = s_hid[ring * 8 + 4] | s_hid[ring * 8 + 5] | s_hid[ring * 8 + 6] |
                                  s_hid[ring * 8 + 7];
-          const bool edge = special || __any_sync(0xffffffffu, hi < KT || lo > 0 || flags != 0u);
-          // 32 scores (times the key's scale; the row's factor follows), hidden ones -inf
-          // (the common case is compiled by itself: branches inside cost it half its rate)
-          auto scores = [&](auto general, uint32_t (&v)[32], int c) {
-            if (!general.value || !special) {
+          const bool general = special || __any_sync(0xffffffffu, hi < KT / 2 || lo > 0 || flags != 0u);
+          tmem_ld_wait();
+          auto scale = [&]() {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const float4 s = sk4[8 * c + e];
-                mul2u(v[4 * e], v[4 * e + 1], s.x, s.y);
-                mul2u(v[4 * e + 2], v[4 * e + 3], s.z, s.w);
+                mul2u(v[c][4 * e], v[c][4 * e + 1], s.x, s.y);
+                mul2u(v[c][4 * e + 2], v[c][4 * e + 3], s.z, s.w);
               }
-            }
-            if (general.value) {
-              const uint32_t seen =
-                  bits_below(hi - 32 * c) & ~bits_below(lo - 32 * c) & ~s_hid[ring * 8 + c];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = (seen & (1u << e)) ? v[e] : 0xFF800000u;
-            }
           };
-          // ---- largest score; the next 32 are on their way while 32 are worked on
-          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto largest = [&](auto general, uint32_t (&v)[32], int c) {
-            scores(general, v, c);
+          if (!special) scale();
+          if (general) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t seen = bits_below(hi - 32 * c) & ~bits_below(lo - 32 * c) &
+                                    ~s_hid[ring * 8 + (key0 >> 5) + c];
 #pragma unroll
-              for (int d = 0; d < 8; d += 2)
-                mx4[e] = fmaxf(mx4[e], fmaxf(__uint_as_float(v[8 * e + d]), __uint_as_float(v[8 * e + d + 1])));
-          };
-          uint32_t va[32], vb[32];
-          tmem_ld32(t_s, va);
-          tmem_ld_wait();
-          if (!edge) {
-#pragma unroll 1
-            for (int c = 0; c < 4; c += 2) {
-              tmem_ld32(t_s + 32 * c + 32, vb);
-              largest(std::false_type(), va, c);
-              tmem_ld_wait();
-              tmem_ld32(t_s + ((32 * c + 64) & 127), va);       // at the end the first again
-              largest(std::false_type(), vb, c + 1);
-              tmem_ld_wait();
-            }
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              largest(std::true_type(), va, c);
-              tmem_ld32(t_s + ((32 * c + 32) & 127), va);
-              tmem_ld_wait();
+              for (int e = 0; e < 32; ++e) v[c][e] = (seen & (1u << e)) ? v[c][e] : 0xFF800000u;
             }
           }
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * ff;
           // ---- references, and the sums rescaled where one has moved far
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+              mx4[d] = fmaxf(mx4[d], fmaxf(__uint_as_float(v[d >> 1][16 * (d & 1) + 2 * e]),
+                                           __uint_as_float(v[d >> 1][16 * (d & 1) + 2 * e + 1])));
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * ff;
           const float4 sm4 = *reinterpret_cast<const float4*>(s_svm + ring * 4);
           const float svmax = fmaxf(fmaxf(sm4.x, sm4.y), fmaxf(sm4.z, sm4.w));
           const bool raise = mx > m + 15.0f || svmax > svr;
@@ -489,8 +487,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
             far = svr > 1.1529215e18f || svr < 8.6736174e-19f;          // 2^60, 2^-60
             mneg = m == -INFINITY ? 0.f : -m;
             if (!far) mneg -= static_cast<float>(static_cast<int>(__float_as_uint(svr) >> 23) - 127);
-            if (i > 0) {
-              ok = __all_sync(0xffffffffu, mbar_wait(&bar.o_full[hf], (mine - 1) & 1, spin));
+            if (j > 0) {
+              ok = __all_sync(0xffffffffu, mbar_wait(&bar.o_full[hf][(mine - 1) & 1], ((mine - 1) >> 1) & 1, spin));
               if (!ok) break;
               tc_fence_after();
               const float g = fa * down;
@@ -508,70 +506,59 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           }
           // ---- weights
           const f2 f2f{ff, ff}, f2m{mneg, mneg};
-          const float svi = svr > 0.f ? 1.0f / svr : 0.f;      // used when far
           f2 sum{0.f, 0.f};
-          auto weights = [&](auto general, uint32_t (&v)[32], int c) {
-            scores(general, v, c);
+          auto weights = [&](auto careful) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              f2 a = fma2(f2{__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])}, f2f, f2m);
-              a = f2{ex2(a.x), ex2(a.y)};
-              sum = add2(sum, a);
-              v[2 * e] = __float_as_uint(a.x);
-              v[2 * e + 1] = __float_as_uint(a.y);
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                f2 a = fma2(f2{__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1])}, f2f, f2m);
+                a = f2{ex2(a.x), ex2(a.y)};
+                sum = add2(sum, a);
+                v[c][2 * e] = __float_as_uint(a.x);
+                v[c][2 * e + 1] = __float_as_uint(a.y);
+              }
+              uint32_t some = 0xffffffffu;
+              if (careful.value) {           // a hidden key's scale may be infinite or NaN
+                some = 0;
+                const float svi = !far ? 1.0f : svr > 0.f ? 1.0f / svr : 0.f;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  some |= (__uint_as_float(v[c][e]) == 0.f ? 0u : 1u) << e;
+                  v[c][e] = __float_as_uint(__uint_as_float(v[c][e]) * svi);
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 s = sv4[8 * c + e];
+                mul2u(v[c][4 * e], v[c][4 * e + 1], s.x, s.y);
+                mul2u(v[c][4 * e + 2], v[c][4 * e + 3], s.z, s.w);
+              }
+              if (careful.value) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[c][e] = (some & (1u << e)) ? v[c][e] : 0u;
+              }
+              uint32_t o[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                o[e] = h2_bits(__floats2half2_rn(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1])));
+              tmem_st16(t_s + 16 * c, o);
             }
-            if (general.value && far) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) mul2u(v[2 * e], v[2 * e + 1], svi, svi);
-            }
-            uint32_t some = 0xffffffffu;
-            if (general.value && (flags & 2u)) {      // some value scale is infinite or NaN: not a hidden key's
-              some = 0;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) some |= (__uint_as_float(v[e]) == 0.f ? 0u : 1u) << e;
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 s = sv4[8 * c + e];
-              mul2u(v[4 * e], v[4 * e + 1], s.x, s.y);
-              mul2u(v[4 * e + 2], v[4 * e + 3], s.z, s.w);
-            }
-            if (general.value && (flags & 2u)) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = (some & (1u << e)) ? v[e] : 0u;
-            }
-            uint32_t o[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              o[e] = h2_bits(__floats2half2_rn(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])));
-            tmem_st16(t_s + 16 * c, o);
           };
-          if (!edge && !far) {
-#pragma unroll 1
-            for (int c = 0; c < 4; c += 2) {
-              tmem_ld32(t_s + 32 * c + 32, vb);
-              tmem_ld_wait();                // before the weights below take the columns' place
-              weights(std::false_type(), va, c);
-              if (c == 0) tmem_ld32(t_s + 64, va);
-              weights(std::false_type(), vb, c + 1);
-              tmem_ld_wait();
-            }
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              weights(std::true_type(), va, c);
-              if (c < 3) tmem_ld32(t_s + 32 * c + 32, va);
-              tmem_ld_wait();
-            }
-          }
+          if (!far && !(flags & 2u))
+            weights(std::false_type());
+          else
+            weights(std::true_type());
           l += (sum.x + sum.y) * (far ? 1.0f : svr);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.p_full[hf]);
+          if (lane == 0) mbar_arrive(&bar.p_full[hf][buf]);
         }
+        // one barrier per buffer: the product two steps back, the last one on the same barrier, is done
+        // once the scores after it are there
         if (ok && n > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&bar.o_full[hf], (mine - 1) & 1, spin));
+          ok = __all_sync(0xffffffffu, mbar_wait(&bar.o_full[hf][(mine - 1) & 1], ((mine - 1) >> 1) & 1, spin));
           tc_fence_after();
         }
       }
@@ -658,31 +645,52 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
         if (bar.last) {
           __threadfence();
           const float* all = P.tpart + static_cast<int64_t>(slot) * P.nsplit * (2 * HALF * (D + 2));
-          for (int q = warp; q < rows; q += 8) {
-            float M = -INFINITY, L = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          constexpr int AT_ONCE = 4;       // rows a warp joins at a time: their loads overlap
+          for (int q0 = warp * AT_ONCE; q0 < rows; q0 += 8 * AT_ONCE) {
+            float M[AT_ONCE], L[AT_ONCE];
+            float4 acc[AT_ONCE];
+#pragma unroll
+            for (int d = 0; d < AT_ONCE; ++d) {
+              M[d] = -INFINITY;
+              L[d] = 0.f;
+              acc[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
             for (int p = 0; p < pieces; ++p) {
               const float* pp = all + static_cast<int64_t>(p) * (2 * HALF * (D + 2));
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(pp + 2 * HALF * D) + q);
-              const float4 o = __ldcg(reinterpret_cast<const float4*>(pp + q * D) + lane);
-              const float nm = fmaxf(M, ml.x);
-              const float fa = M == -INFINITY ? 0.f : ex2(M - nm);
-              const float fb = ml.x == -INFINITY ? 0.f : ex2(ml.x - nm);
-              M = nm;
-              L = L * fa + ml.y * fb;
-              acc.x = acc.x * fa + (fb != 0.f ? o.x * fb : 0.f);
-              acc.y = acc.y * fa + (fb != 0.f ? o.y * fb : 0.f);
-              acc.z = acc.z * fa + (fb != 0.f ? o.z * fb : 0.f);
-              acc.w = acc.w * fa + (fb != 0.f ? o.w * fb : 0.f);
+              float2 ml[AT_ONCE];
+              float4 o[AT_ONCE];
+#pragma unroll
+              for (int d = 0; d < AT_ONCE; ++d) {
+                const int q = min(q0 + d, rows - 1);
+                ml[d] = __ldcg(reinterpret_cast<const float2*>(pp + 2 * HALF * D) + q);
+                o[d] = __ldcg(reinterpret_cast<const float4*>(pp + q * D) + lane);
+              }
+#pragma unroll
+              for (int d = 0; d < AT_ONCE; ++d) {
+                const float nm = fmaxf(M[d], ml[d].x);
+                const float fa = M[d] == -INFINITY ? 0.f : ex2(M[d] - nm);
+                const float fb = ml[d].x == -INFINITY ? 0.f : ex2(ml[d].x - nm);
+                M[d] = nm;
+                L[d] = L[d] * fa + ml[d].y * fb;
+                acc[d].x = acc[d].x * fa + (fb != 0.f ? o[d].x * fb : 0.f);
+                acc[d].y = acc[d].y * fa + (fb != 0.f ? o[d].y * fb : 0.f);
+                acc[d].z = acc[d].z * fa + (fb != 0.f ? o[d].z * fb : 0.f);
+                acc[d].w = acc[d].w * fa + (fb != 0.f ? o[d].w * fb : 0.f);
+              }
             }
-            const int tq = (u.base + q) / P.G, hq_ = u.h * P.G + u.base + q - tq * P.G;
-            const int64_t orow = static_cast<int64_t>(u.row0 + tq) * P.hq + hq_;
-            const float inv = L == 0.f ? 0.f : 1.0f / L;
-            __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-            __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-            *reinterpret_cast<uint2*>(P.out + orow * D + 4 * lane) =
-                make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
-            if (P.lse && lane == 0) P.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+#pragma unroll
+            for (int d = 0; d < AT_ONCE; ++d) {
+              const int q = q0 + d;
+              if (q >= rows) continue;
+              const int tq = (u.base + q) / P.G, hq_ = u.h * P.G + u.base + q - tq * P.G;
+              const int64_t orow = static_cast<int64_t>(u.row0 + tq) * P.hq + hq_;
+              const float inv = L[d] == 0.f ? 0.f : 1.0f / L[d];
+              __nv_bfloat162 a = __floats2bfloat162_rn(acc[d].x * inv, acc[d].y * inv);
+              __nv_bfloat162 b = __floats2bfloat162_rn(acc[d].z * inv, acc[d].w * inv);
+              *reinterpret_cast<uint2*>(P.out + orow * D + 4 * lane) =
+                  make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+              if (P.lse && lane == 0) P.lse[orow] = L[d] == 0.f ? -INFINITY : (M[d] + log2f(L[d])) * kLn2;
+            }
           }
         }
         __syncwarp();                      // bar.last has been read: the next unit's write waits for
@@ -692,7 +700,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
     }
   } else if (warp < 12) {
     // ----------------------------------------------------------- widening
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(BITS == 4 ? 88 : 104));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(104));
     const int pw = warp - 8, t = lane & 3, b3 = lane >> 2;
     // rows of a warp's load instruction; the two rows of a store phase differ in a bit that the
     // lanes' chunks do not use (see widen_rows)
@@ -818,31 +826,33 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
     }
   } else {
     // ------------------------------------------------------------ products
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 12) {
-    int tiles = 0, seen = 0, qs = 0;         // seen, qs: bit h, the parity that half h waits for next
+    int tiles = 0, qs = 0, cnt = 0;          // qs: bit h, half h's parity; cnt: 2 bits, its steps so far
     const uint64_t q_desc = desc_sw128(smem_u32(smem + OFF_Q)), k_desc = desc_sw128(smem_u32(smem + OFF_K)),
                    v_desc = desc_sw128_mn(smem_u32(smem + OFF_V), PANEL, 1024);
     for (int k = 0; ok; ++k) {
       ok = __all_sync(0xffffffffu, mbar_wait(&bar.u_full[k % UNITS], (k / UNITS) & 1, spin));
       if (!ok) break;
       const volatile TileUnit& u = ring_u[k % UNITS];
-      const int rows = u.rows, n = u.n;
+      const int rows = u.rows, n = u.n, steps = u.steps;
       if (rows == 0) break;
       const int halves = rows > HALF ? 2 : 1;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.u_free[k % UNITS]);
       // descriptors advance by constants in their low word (addresses / 16): few registers
-      auto scores = [&](int h, int tile) {
+      auto scores = [&](int h, int j, int buf) {
         if (lane == 0) {
-          const uint64_t a = q_desc + ((h * 2 * PANEL) >> 4), b = k_desc + (((tile & 1) * 2 * PANEL) >> 4);
+          const int stage = (tiles + (j >> 1)) & 1;
+          const uint64_t a = q_desc + ((h * 2 * PANEL) >> 4),
+                         b = k_desc + ((stage * 2 * PANEL + (j & 1) * (PANEL / 2)) >> 4);
 #pragma unroll
           for (int s = 0; s < 8; ++s) {
             const uint32_t off = ((s >> 2) * PANEL + (s & 3) * 32) >> 4;
-            mma_f16_ss(tmem + h * 128, a + off, b + off, IDESC_S, s > 0);
+            mma_f16_ss(tmem + h * 128 + buf * (KT / 2), a + off, b + off, IDESC_S, s > 0);
           }
-          mma_commit(&bar.s_full[h]);
-          if (h == halves - 1) mma_commit(&bar.k_free[tile & 1]);
+          mma_commit(&bar.s_full[h][buf]);
+          if (h == halves - 1 && ((j & 1) || j == steps - 1)) mma_commit(&bar.k_free[stage]);
         }
         __syncwarp();
       };
@@ -854,39 +864,44 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      if (n > 0)
+      // two steps of scores ahead: a half's next scores are there when its softmax ends
 #pragma unroll 1
-        for (int h = 0; h < halves; ++h) scores(h, tiles);
-      for (int i = 0; i < n && ok; ++i, ++tiles) {
+      for (int j = 0; j < min(steps, 2); ++j)
+#pragma unroll 1
+        for (int h = 0; h < halves; ++h) scores(h, j, ((cnt >> (2 * h)) + j) & 1);
+      for (int j = 0; j < steps && ok; ++j) {
+        const int tile = tiles + (j >> 1);
 #pragma unroll 1
         for (int h = 0; h < halves && ok; ++h) {
-          ok = mbar_wait(&bar.p_full[h], (seen >> h) & 1, spin);
-          seen ^= 1 << h;
-          if (ok && h == 0) ok = mbar_wait(&bar.v_full[tiles & 1], (tiles >> 1) & 1, spin);
+          const int c = (cnt >> (2 * h)) & 3, buf = c & 1;
+          ok = mbar_wait(&bar.p_full[h][buf], c >> 1, spin);
+          cnt = (cnt & ~(3 << (2 * h))) | (((c + 1) & 3) << (2 * h));
+          if (ok && h == 0 && !(j & 1)) ok = mbar_wait(&bar.v_full[tile & 1], (tile >> 1) & 1, spin);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           if (lane == 0) {
-            const uint64_t b = v_desc + (((tiles & 1) * 2 * PANEL) >> 4);
+            const uint64_t b = v_desc + (((tile & 1) * 2 * PANEL + (j & 1) * (PANEL / 2)) >> 4);
 #pragma unroll
-            for (int s = 0; s < 8; ++s)
-              mma_f16_ts(tmem + 256 + h * 128, tmem + h * 128 + 8 * s, b + s * (2048 >> 4), IDESC_O,
-                         i > 0 || s > 0);
-            mma_commit(&bar.o_full[h]);
-            if (h == halves - 1) mma_commit(&bar.v_free[tiles & 1]);
+            for (int s = 0; s < 4; ++s)
+              mma_f16_ts(tmem + 256 + h * 128, tmem + h * 128 + buf * (KT / 2) + 8 * s, b + s * (2048 >> 4),
+                         IDESC_O, j > 0 || s > 0);
+            mma_commit(&bar.o_full[h][buf]);
+            if (h == halves - 1 && ((j & 1) || j == steps - 1)) mma_commit(&bar.v_free[tile & 1]);
           }
           __syncwarp();
-          if (i + 1 < n) {
-            if (h == 0) {
+          if (j + 2 < steps) {
+            if (h == 0 && !(j & 1)) {
               ok = __all_sync(0xffffffffu,
-                              mbar_wait(&bar.k_full[(tiles + 1) & 1], ((tiles + 1) >> 1) & 1, spin));
+                              mbar_wait(&bar.k_full[(tile + 1) & 1], ((tile + 1) >> 1) & 1, spin));
               if (!ok) break;
               tc_fence_after();
             }
-            scores(h, tiles + 1);
+            scores(h, j + 2, buf);
           }
         }
       }
+      tiles += n;
     }
     // no product may still write the tensor memory freed below
     if (lane == 0) {
