@@ -40,7 +40,7 @@
 // weights move from S^T's accumulator layout to the B operand by movmatrix.
 //
 // Work split: the key tiles of all (sequence, row block, KV head) units form
-// one list and every CTA takes an equal contiguous piece.  A unit cut between
+// one list and every CTA takes a contiguous piece of it.  A unit cut between
 // CTAs leaves partial (O, m, l) in the workspace; the last CTA to arrive adds
 // them in the order of the list, so results do not depend on arrival order.
 #include <cuda_bf16.h>
@@ -96,6 +96,8 @@ struct Unit {
   Seq s;
   int b, h, row0, rows;                    // row0: first of its (token, head) rows
 };
+
+constexpr int kOverhead = 4;               // tiles that a unit's beginning and end cost
 
 template <int BITS, int NT, bool PAIR>
 struct Stream {
@@ -193,8 +195,7 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
   extern __shared__ __align__(128) uint8_t stream_smem[];
   auto sm_o = [&](int w) { return reinterpret_cast<float(*)[D]>(stream_smem + w * St::RING); };
   __shared__ float sm_m[WARPS][R], sm_l[WARPS][R], sm_f[THREADS], sm_fl[THREADS], sm_top[R];
-  __shared__ int64_t sm_scan[WARPS];
-  __shared__ int64_t sm_total, sm_base;
+  __shared__ int64_t sm_scan[2 * WARPS], sm_base;
   __shared__ int sm_b;
   __shared__ bool sm_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -202,16 +203,48 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
   const bool split = P.part != nullptr;
 
   // ---- the list: this CTA's piece, and the sequence it begins in
-  auto weight = [&](const Seq& s, int& per) {
-    const int nrt = s.qlen * G > P.many_rows ? 0 : (s.qlen * G + R - 1) / R;
-    per = split ? max(s.tiles(), 1) : 1;   // tiles per unit; a unit without keys still writes zeros
-    return static_cast<int64_t>(nrt) * hkv * per;
+  auto count = [&](const Seq& s) {         // units of a sequence
+    return s.qlen * G > P.many_rows ? 0ll : static_cast<long long>((s.qlen * G + R - 1) / R) * hkv;
   };
-  const int chunk = (B + THREADS - 1) / THREADS;
+  const int chunk = (B + THREADS - 1) / THREADS, bfirst = tid * chunk, blast = min(B, bfirst + chunk);
+  // Few units (a decode step of long sequences): each gets CTAs of its own, as many as share its tiles
+  // evenly, since a CTA that ends one unit and begins another pays twice for a unit's beginning and
+  // end (6 of 84 us for two 131k documents).  Many: all get equal pieces of the list of tiles, where
+  // a unit's beginning and end count as kOverhead tiles (a batch of ragged lengths would else leave
+  // the CTAs with the short ones behind: 101 against 62 us).
+  int64_t tiles = 0, units = 0;
+  for (int b = bfirst; b < blast; ++b) {
+    const Seq s = load_seq(P, b, blockIdx.x == 0);
+    units += count(s);
+    tiles += count(s) * max(s.tiles(), 1);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    units += __shfl_xor_sync(0xffffffffu, units, o);
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+  }
+  if (lane == 0) {
+    sm_scan[warp] = units;
+    sm_scan[WARPS + warp] = tiles;
+  }
+  __syncthreads();
+  units = tiles = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    units += sm_scan[w];
+    tiles += sm_scan[WARPS + w];
+  }
+  const bool slots = split && 2 * units <= gridDim.x;
+  const int per_slot = slots ? static_cast<int>(min(tiles / (gridDim.x - units) + 1, static_cast<int64_t>(1 << 30))) : 1;
+  // places of a unit in the list: slots, or tiles behind kOverhead; a unit without keys still writes zeros
+  auto places = [&](const Seq& s) {
+    const int n = max(s.tiles(), 1);
+    return !split ? 1 : slots ? (n + per_slot - 1) / per_slot : n + kOverhead;
+  };
   int64_t mine = 0;
-  for (int b = tid * chunk; b < min(B, (tid + 1) * chunk); ++b) {
-    int per;
-    mine += weight(load_seq(P, b, blockIdx.x == 0), per);
+  for (int b = bfirst; b < blast; ++b) {
+    const Seq s = load_seq(P, b, false);
+    mine += count(s) * places(s);
   }
   int64_t incl = mine;
 #pragma unroll
@@ -219,6 +252,7 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
     const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
+  __syncthreads();
   if (lane == 31) sm_scan[warp] = incl;
   __syncthreads();
   int64_t before = 0, total = 0;
@@ -229,15 +263,15 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
   }
   const int64_t excl = before + incl - mine;
   // equal pieces but for the last; a unit's pieces belong to consecutive CTAs
-  const int64_t piece = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t piece = slots ? 1 : (total + gridDim.x - 1) / gridDim.x;
   const int64_t r0 = piece * blockIdx.x, r1 = min(total, r0 + piece);
   if (r0 >= r1) return;
   if (r0 >= excl && r0 < excl + mine) {
-    int b = tid * chunk;
+    int b = bfirst;
     int64_t base = excl;
     for (;; ++b) {
-      int per;
-      const int64_t w = weight(load_seq(P, b, false), per);
+      const Seq s = load_seq(P, b, false);
+      const int64_t w = count(s) * places(s);
       if (r0 < base + w) break;
       base += w;
     }
@@ -251,24 +285,111 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
   for (int64_t cur = r0; cur < r1;) {
     Unit u;
     u.s = load_seq(P, b, false);
-    int per;
-    const int64_t wgt = weight(u.s, per);
+    const int per = places(u.s), all = u.s.tiles();
+    const int64_t wgt = count(u.s) * per;
     if (cur >= base + wgt) {
       base += wgt;
       ++b;
       continue;
     }
-    const int64_t unit = (cur - base) / per;
+    int64_t unit;
+    if (wgt >> 31 == 0)
+      unit = static_cast<uint32_t>(cur - base) / static_cast<uint32_t>(per);
+    else
+      unit = (cur - base) / per;
     const int i0 = static_cast<int>((cur - base) - unit * per);
     const int i1 = static_cast<int>(min(static_cast<int64_t>(per), i0 + (r1 - cur)));
     const int64_t u0 = base + unit * per;  // the unit's place in the list
-    const bool whole = i0 == 0 && i1 == per;
-    u.b = b;
-    u.h = static_cast<int>(unit % hkv);
-    u.row0 = static_cast<int>(unit / hkv) * R;
-    u.rows = min(R, u.s.qlen * G - u.row0);
     cur += i1 - i0;
-    const int first = split ? i0 : 0, last = split ? min(i1, u.s.tiles()) : u.s.tiles();
+    // this CTA's tiles of the unit, and the CTAs that have any
+    int first = 0, last = all;
+    int64_t c0 = 0, c1 = 0;
+    if (slots) {
+      first = static_cast<int>(static_cast<int64_t>(all) * i0 / per);
+      last = static_cast<int>(static_cast<int64_t>(all) * i1 / per);
+      c0 = u0;
+      c1 = u0 + per - 1;
+    } else if (split) {
+      const int lead = per - max(all, 1);
+      first = max(i0 - lead, 0);
+      last = i1 - lead;
+      if (last <= first) continue;         // the unit's overhead alone
+      last = min(last, all);
+      if (first > 0 || last < all) {
+        c0 = (u0 + lead) / piece;
+        c1 = (u0 + per - 1) / piece;
+      }
+    }
+    const bool whole = c0 == c1;
+    u.b = b;
+    u.row0 = wgt >> 31 == 0 ? static_cast<int>(static_cast<uint32_t>(unit) / static_cast<uint32_t>(hkv))
+                            : static_cast<int>(unit / hkv);
+    u.h = static_cast<int>(unit - static_cast<int64_t>(u.row0) * hkv);
+    u.row0 *= R;
+    u.rows = min(R, u.s.qlen * G - u.row0);
+
+    // ---- the way of 32 keys into the ring: the shared prefix's tiles that are this CTA's (where no
+    // other kernel takes them), then the own
+    const uint8_t* ring = stream_smem + warp * St::RING;
+    const uint32_t ring32 = smem_u32(ring);
+    // lanes 0..3 fetch a group's K scales, 4..7 its V scales, 8 and 9 its zero points
+    const uint8_t* extra = reinterpret_cast<const uint8_t*>(lane < 4 ? P.pages.ks : P.pages.vs) + 16 * (lane & 3);
+    if (lane == 8) extra = P.pages.kz;
+    if (lane == 9) extra = P.pages.vz;
+    const int extra_step = lane < 8 ? 4 : 1;
+    const int in_page = (1 << P.pages.lps) - 1;
+    int local, end, limit, kshift, pg[2];
+    const int32_t* table;
+    // pages of both groups of 16, -1: no keys
+    auto pages_of = [&](int row, int (&to)[2]) {
+      to[0] = row < end ? __ldg(table + (row >> P.pages.lps)) : -1;
+      to[1] = row + 16 < end ? __ldg(table + ((row + 16) >> P.pages.lps)) : -1;
+    };
+    unsigned there = 0;                    // bits 2 slot + group: it holds keys
+    auto fetch = [&](int from, const int (&pages)[2], int slot) {
+      there &= ~(3u << (2 * slot));
+#pragma unroll
+      for (int gr = 0; gr < 2; ++gr) {
+        const int row = from + 16 * gr;
+        if (row < end) {
+          if (pages[gr] < 0 || pages[gr] >= P.pages.num_pages) {
+            if (lane == 0) record_status(SQ_ERR_INVALID_ARG);
+          } else {
+            const int64_t grp = group_of(P.pages, pages[gr], u.h, row & in_page);
+            const uint32_t dst = ring32 + slot * St::SLOT + gr * St::GROUP;
+            const uint8_t* kc = P.pages.kc + grp * RB + 16 * lane;
+            const uint8_t* vc = P.pages.vc + grp * RB + 16 * lane;
+            constexpr int CPR = RB / 16, RPI = 32 / CPR;         // chunks per row, rows per instruction
+#pragma unroll
+            for (int j = 0; j < 16 / RPI; ++j) {
+              const int rw = j * RPI + lane / CPR, c = lane % CPR;
+              cp_async16(dst + St::k_at(rw, c), kc + 512 * j);
+              cp_async16(dst + St::V0 + St::v_at(rw, c), vc + 512 * j);
+            }
+            if (lane < 10) cp_async16(dst + St::SC0 + 16 * lane, extra + grp * extra_step);
+            there |= 1u << (2 * slot + gr);
+          }
+        }
+      }
+      cp_async_commit();
+    };
+    auto begin = [&](int seg) {            // a segment's first two slots on their way
+      const int t0 = seg ? u.s.ot0 + max(first - u.s.pn, 0) : u.s.pt0 + first;
+      const int t1 = seg ? u.s.ot0 + last - u.s.pn : u.s.pt0 + min(last, u.s.pn);
+      limit = seg ? u.s.len : P.prefix_len;
+      kshift = seg ? P.prefix_len : 0;
+      table = seg ? P.batch.table + static_cast<int64_t>(u.b) * P.batch.width : P.prefix_table;
+      end = min(limit, t1 * TILE);
+      local = t0 * TILE + 32 * warp;
+      int next[2];
+      pages_of(local, pg);
+      pages_of(local + TILE, next);
+      fetch(local, pg, 0);
+      fetch(local + TILE, next, 1);
+      pages_of(local + 2 * TILE, pg);
+    };
+    const int seg0 = first < u.s.pn ? 0 : 1;
+    begin(seg0);
 
     uint32_t qb[NT][8][2];
     float qf[NT][2], qs[NT][2];
@@ -303,64 +424,9 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
     for (int n = 0; n < NT; ++n) ff[n][0] = special ? 1.f : qf[n][0], ff[n][1] = special ? 1.f : qf[n][1];
     float svr = 0.f, svi = 0.f;            // power of two at or above the value scales so far; 1 / svr
 
-    const uint8_t* ring = stream_smem + warp * St::RING;
-    const uint32_t ring32 = smem_u32(ring);
-    // lanes 0..3 fetch a group's K scales, 4..7 its V scales, 8 and 9 its zero points
-    const uint8_t* extra = reinterpret_cast<const uint8_t*>(lane < 4 ? P.pages.ks : P.pages.vs) + 16 * (lane & 3);
-    if (lane == 8) extra = P.pages.kz;
-    if (lane == 9) extra = P.pages.vz;
-    const int extra_step = lane < 8 ? 4 : 1;
-    const int in_page = (1 << P.pages.lps) - 1;
-
-    // the shared prefix's tiles that are this CTA's (where no other kernel takes them), then the own
 #pragma unroll 1
-    for (int seg = first < u.s.pn ? 0 : 1; seg < 2; ++seg) {
-      const int t0 = seg ? u.s.ot0 + max(first - u.s.pn, 0) : u.s.pt0 + first;
-      const int t1 = seg ? u.s.ot0 + last - u.s.pn : u.s.pt0 + min(last, u.s.pn);
-      const int limit = seg ? u.s.len : P.prefix_len, kshift = seg ? P.prefix_len : 0;
-      const int32_t* table = seg ? P.batch.table + static_cast<int64_t>(u.b) * P.batch.width : P.prefix_table;
-      const int end = min(limit, t1 * TILE);
-      // ---- the way of 32 keys into the ring; pages of both groups, -1: no keys
-      auto pages_of = [&](int local, int (&pg)[2]) {
-        pg[0] = local < end ? __ldg(table + (local >> P.pages.lps)) : -1;
-        pg[1] = local + 16 < end ? __ldg(table + ((local + 16) >> P.pages.lps)) : -1;
-      };
-      unsigned there = 0;                  // bits 2 slot + group: it holds keys
-      auto fetch = [&](int local, const int (&pg)[2], int slot) {
-        there &= ~(3u << (2 * slot));
-#pragma unroll
-        for (int gr = 0; gr < 2; ++gr) {
-          const int row = local + 16 * gr;
-          if (row < end) {
-            if (pg[gr] < 0 || pg[gr] >= P.pages.num_pages) {
-              if (lane == 0) record_status(SQ_ERR_INVALID_ARG);
-            } else {
-              const int64_t grp = group_of(P.pages, pg[gr], u.h, row & in_page);
-              const uint32_t dst = ring32 + slot * St::SLOT + gr * St::GROUP;
-              const uint8_t* kc = P.pages.kc + grp * RB + 16 * lane;
-              const uint8_t* vc = P.pages.vc + grp * RB + 16 * lane;
-              constexpr int CPR = RB / 16, RPI = 32 / CPR;       // chunks per row, rows per instruction
-#pragma unroll
-              for (int j = 0; j < 16 / RPI; ++j) {
-                const int rw = j * RPI + lane / CPR, c = lane % CPR;
-                cp_async16(dst + St::k_at(rw, c), kc + 512 * j);
-                cp_async16(dst + St::V0 + St::v_at(rw, c), vc + 512 * j);
-              }
-              if (lane < 10) cp_async16(dst + St::SC0 + 16 * lane, extra + grp * extra_step);
-              there |= 1u << (2 * slot + gr);
-            }
-          }
-        }
-        cp_async_commit();
-      };
-      int local = t0 * TILE + 32 * warp;
-      int pg[2], pn[2];
-      pages_of(local, pg);
-      pages_of(local + TILE, pn);
-      fetch(local, pg, 0);
-      fetch(local + TILE, pn, 1);
-      pages_of(local + 2 * TILE, pg);
-
+    for (int seg = seg0; seg < 2; ++seg) {
+      if (seg != seg0) begin(seg);
       for (int slot = 0; local < end; local += TILE, slot ^= 1) {
         cp_async_wait<St::DEPTH - 1>();
         __syncwarp();
@@ -643,10 +709,11 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
     // largest reference first, then 128 / R pieces' factors at a time by one thread each, so that
     // every load but the factors' is independent
     auto join = [&](int n, auto ml, auto out) {
-      constexpr int STEP = THREADS / R, AHEAD = 32 / R;
+      constexpr int STEP = THREADS / R, AHEAD = 64 / R;
       const int jr = tid % R, jq = tid / R;
-      float top = -INFINITY;
-      for (int q = jq; q < n; q += STEP) top = fmaxf(top, ml(q, jr).x);
+      const float2 mine = jq < n ? ml(jq, jr) : make_float2(-INFINITY, 0.f);
+      float top = mine.x;
+      for (int q = jq + STEP; q < n; q += STEP) top = fmaxf(top, ml(q, jr).x);
       sm_f[tid] = top;
       __syncthreads();
 #pragma unroll
@@ -664,7 +731,7 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
         const int q = q0 + jq;
         float f = 0.f, fl = 0.f;
         if (q < n) {
-          const float2 v = ml(q, jr);
+          const float2 v = q0 == 0 ? mine : ml(q, jr);
           f = v.x == -INFINITY ? 0.f : ex2(v.x - sm_top[jr]);
           fl = f * v.y;
         }
@@ -693,7 +760,6 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
       __syncthreads();
     };
     if (!whole) {
-      const int64_t c0 = u0 / piece, c1 = (u0 + per - 1) / piece;      // CTAs of its first and last tile
       float* p = P.part + static_cast<int64_t>(part) * PART;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
