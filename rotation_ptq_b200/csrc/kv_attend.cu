@@ -97,7 +97,7 @@ struct Unit {
   int b, h, row0, rows;                    // row0: first of its (token, head) rows
 };
 
-constexpr int kOverhead = 4;               // tiles that a unit's beginning and end cost
+constexpr int kOverhead = 3;               // tiles that a unit's beginning and end cost
 
 template <int BITS, int NT, bool PAIR>
 struct Stream {

@@ -3,17 +3,21 @@
 //
 // A unit is up to 256 rows (token, query head of one KV head) in two halves of
 // 128, and a run of 128-key tiles.  Per half and tile
-//     S = Q K_int^T            (tensor memory, f32; Q and codes exact in fp16), in two steps of 64 keys
+//     S = Q K_int^T            (tensor memory, f32; Q and codes exact in fp16)
 //     y = S sk,  p = exp2(y f_row - m),  P = fp16(p sv)      (tensor memory)
 //     O += P V_int             (A from tensor memory, f32)
 // with K_int, V_int the codes less their zero points.  The row scales sk and
 // sv stay outside the products, so fp16 operands lose nothing; P is rounded
 // once to 11 bits, an eighth of what the bf16 output's own rounding may lose.
 //
-// Warps: 0-3 and 4-7 softmax of half 0 and 1 (a thread per row: no exchange
-// between lanes), 8-11 widen codes from global memory into swizzled shared
-// memory, 12 issues the products, 13 works out the units.  Each half has two buffers of 64
-// scores: the products of a step run while the softmax of the step before does.
+// Warps: 0-3 and 4-7 softmax of half 0 and 1 (in the fragment layout: a
+// lane needs the scales of a quarter of the keys.  With a thread per row every
+// lane reads them all, and those reads and the products' operands stand in one
+// another's way in shared memory: the softmax took 1.7 times as long), 8-11 widen codes from global memory into swizzled shared
+// memory, 12 and 13 issue the halves' products, 14 works out
+// the units.  A step is 64 keys and
+// each half has two buffers of scores, so that the next step's scores are there when a softmax ends;
+// the halves run independently.
 //
 // Two rows of work: a sequence's own rows over what it sees (splits of a
 // unit's tiles are joined by the last CTA to arrive, in order), or, for a
@@ -33,7 +37,7 @@ namespace paged {
 
 constexpr int KT = 128;                    // keys per tile
 constexpr int HALF = 128;                  // rows per half
-constexpr int TILE_THREADS = 16 * 32;    // warps 14 and 15 fill the last group
+constexpr int TILE_THREADS = 16 * 32;    // warp 15 fills the last group
 constexpr int UNITS = 3;                   // unit records in flight
 constexpr int PANEL = 128 * 128;           // bytes of 128 rows x 64 fp16
 constexpr int OFF_Q = 0;                   // [half][2 panels]
@@ -46,38 +50,60 @@ constexpr int OFF_SVM = OFF_HID + 128;         // float [4][4]: largest value sc
 constexpr int OFF_BARS = OFF_SVM + 64;
 constexpr int OFF_UNITS = OFF_BARS + 512;      // TileUnit [UNITS]
 constexpr int TILE_SMEM = OFF_UNITS + UNITS * 128 + 1024;
-constexpr uint32_t TILE_TMEM = 512;        // S [half][buffer] of 64 columns, O [half] of 128
+constexpr uint32_t TILE_TMEM = 512;        // S [half][64 keys], O [half]
 constexpr uint32_t IDESC_S = idesc_f16(128, KT / 2, false, false);
+// A row's reference is its largest score so far less kTop (log2 units): weights reach 2^kTop and may
+// pass it by kSlack more before the sums are rescaled (which costs as much as the rest of a step;
+// with a slack of 1 it came in most of a prompt's steps).  fp16 then holds weights in full down to
+// 2^-(14 + kTop) of the largest and in fixed steps of 2^-(24 + kTop) below.
+constexpr float kTop = 10.0f, kSlack = 5.0f;
 constexpr uint32_t IDESC_O = idesc_f16(128, 128, false, true);
 
 struct TileBars {
   uint64_t k_full[2], v_full[2], k_free[2], v_free[2], sc_full[4];
-  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2];        // s, p, o: [half][buffer]
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2];        // [half][the tile's first or second 64 keys]
   uint64_t parts, joined, drain;           // partial results written; who joins them is known
   uint64_t u_full[UNITS], u_free[UNITS];
   uint32_t tmem, last;
 };
 static_assert(sizeof(TileBars) <= 512, "barriers");
 
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+// Products and commits under a predicate (the elected lane): the issuing warps' code stays uniform, so
+// that descriptors are computed once for the warp and cost no moves (a branch around the products made
+// a step of 12 take 1500 cycles to issue).
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+
+__device__ __forceinline__ void mma_f16_ss(uint32_t elected, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                            uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(elected)
       : "memory");
 }
 
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_f16_ts(uint32_t elected, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                            uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(elected)
       : "memory");
 }
 
-// A unit as every role sees it.  Warp 13 works them out and hands them on in a ring of records in
+__device__ __forceinline__ void commit_if(uint32_t elected, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar)), "r"(elected)
+      : "memory");
+}
+
+// A unit as every role sees it.  Warp 14 works them out and hands them on in a ring of records in
 // shared memory: the other roles hold only what they use.  rows 0: no unit follows.
 struct TileUnit {
   int row0;                                // packed row of the first token
@@ -219,6 +245,51 @@ __device__ __forceinline__ void mul2u(uint32_t& a, uint32_t& b, float x, float y
   b = __float_as_uint(r.y);
 }
 
+// Tensor memory in the fragment layout, 16 lanes (rows) at a time.  Lane (g, t) = (lane / 4, lane % 4)
+// of the warp holds, of every group of 8 columns, columns 2t, 2t + 1 of row g (registers 4 i, 4 i + 1
+// of group i) and of row g + 8 (4 i + 2, 4 i + 3); of 16-bit pairs, every group of 4 columns, column t
+// of row g (2 i) and of row g + 8 (2 i + 1).
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_16x256b_x1(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x256b_x1(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+
 // ------------------------------------------------------------ widening
 
 template <int BITS>
@@ -228,14 +299,15 @@ struct TileCodes {                         // a producer lane's share of one ope
 
 template <int BITS>
 __device__ __forceinline__ void widen_rows(uint8_t* dst, const TileCodes<BITS>& v,
-                                           const int (&zero)[4], int warp_row, int rsub, int t) {
+                                           int zeros, int warp_row, int rsub, int t) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int row = warp_row + 8 * j + rsub;
-    const __half2 z1 = __half2half2(__int2half_rn(-1024 - zero[j]));
+    const uint32_t zero = __shfl_sync(0xffffffffu, zeros, 8 * j + rsub);  // of lane's row: warp_row + lane
+    const __half2 z1 = bits_h2((zero * 0x00010001u) | 0xE400E400u);       // -(1024 + zero)
     uint8_t* line = dst + row * 128;
     if (BITS == 4) {
-      const __half2 z16 = __half2half2(__int2half_rn(-64 - zero[j]));
+      const __half2 z16 = bits_h2((zero * 0x00100010u) | 0xD400D400u);    // -(64 + zero)
       const uint32_t w[4] = {v.c[j][0].x, v.c[j][0].y, v.c[j][0].z, v.c[j][0].w};
       const int odd = t >> 1;
 #pragma unroll
@@ -267,6 +339,95 @@ __device__ __forceinline__ void widen_rows(uint8_t* dst, const TileCodes<BITS>& 
   }
 }
 
+// The products of half H, by one warp.  Tensor memory is the whole SM's (512 columns), so its address is 0.
+template <int H>
+__device__ __forceinline__ void issue_products(const AttnParams& P, uint8_t* smem, TileBars& bar,
+                                               const TileUnit* ring_u) {
+  constexpr uint32_t t_s = H * 128, t_o = 256 + H * 128;
+  const uint32_t spin = P.spin_limit, elected = elect_lane();
+  bool ok = true;
+  int tiles = 0;
+  uint32_t par_q = 0, par_p = 0;           // parities that come next: q_full; bit b, p_full[b]
+  const uint64_t q_desc = desc_sw128(smem_u32(smem + OFF_Q) + H * 2 * PANEL),
+                 k_desc = desc_sw128(smem_u32(smem + OFF_K)),
+                 v_desc = desc_sw128_mn(smem_u32(smem + OFF_V), PANEL, 1024);
+  for (int k = 0, slot = 0, par_u = 0; ok; ++k) {
+    ok = __all_sync(0xffffffffu, mbar_wait(&bar.u_full[slot], par_u, spin));
+    if (!ok) break;
+    const volatile TileUnit& u = ring_u[slot];
+    const int rows = __shfl_sync(0xffffffffu, u.rows, 0), n = __shfl_sync(0xffffffffu, u.n, 0),
+              steps = __shfl_sync(0xffffffffu, u.steps, 0);
+    if (rows == 0) break;
+    __syncwarp();
+    if (elected) mbar_arrive(&bar.u_free[slot]);
+    if (++slot == UNITS) slot = 0, par_u ^= 1;
+    if (H * HALF >= rows) {
+      // a half without rows lets go of the tiles as they come
+      for (int i = 0; i < n && ok; ++i) {
+        const int tile = tiles + i;
+        ok = mbar_wait(&bar.k_full[tile & 1], (tile >> 1) & 1, spin);
+        if (ok && elected) mbar_arrive(&bar.k_free[tile & 1]);
+        ok = ok && mbar_wait(&bar.v_full[tile & 1], (tile >> 1) & 1, spin);
+        if (ok && elected) mbar_arrive(&bar.v_free[tile & 1]);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      tiles += n;
+      continue;
+    }
+    ok = __all_sync(0xffffffffu, mbar_wait(&bar.q_full[H], par_q, spin));
+    par_q ^= 1;
+    // scores of step j, whose tile is there; they run two steps (the buffers) ahead of the products
+    // with values
+    auto scores = [&](int j) {
+      const int stage = (tiles + (j >> 1)) & 1, b = j & 1;
+      const uint64_t kd = k_desc + ((stage * 2 * PANEL + b * (PANEL / 2)) >> 4);
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const uint32_t off = ((s >> 2) * PANEL + (s & 3) * 32) >> 4;
+        mma_f16_ss(elected, t_s + b * (KT / 2), q_desc + off, kd + off, IDESC_S, s > 0);
+      }
+      commit_if(elected, &bar.s_full[H][b]);
+      if (b || j == steps - 1) commit_if(elected, &bar.k_free[stage]);
+    };
+    if (ok && steps > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar.k_full[tiles & 1], (tiles >> 1) & 1, spin));
+      tc_fence_after();
+      if (ok) {
+        scores(0);
+        if (steps > 1) scores(1);
+      }
+    }
+    for (int j = 0; j < steps && ok; ++j) {
+      const int tile = tiles + (j >> 1), stage = tile & 1, b = j & 1;
+      ok = mbar_wait(&bar.p_full[H][b], (par_p >> b) & 1, spin);
+      par_p ^= 1u << b;
+      if (b == 0) ok = ok && mbar_wait(&bar.v_full[stage], (tile >> 1) & 1, spin);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t vd = v_desc + ((stage * 2 * PANEL + b * (PANEL / 2)) >> 4);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        mma_f16_ts(elected, t_o, t_s + b * (KT / 2) + 8 * s, vd + s * (2048 >> 4), IDESC_O, j > 0 || s > 0);
+      commit_if(elected, &bar.o_full[H][b]);
+      if (b || j == steps - 1) commit_if(elected, &bar.v_free[stage]);
+      if (j + 2 < steps) {
+        if (b == 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&bar.k_full[stage ^ 1], ((tile + 1) >> 1) & 1, spin));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        scores(j + 2);
+      }
+    }
+    tiles += n;
+  }
+  // no product may still write the tensor memory freed when all have left
+  commit_if(elected, &bar.drain);
+  mbar_wait(&bar.drain, 0, 0);
+  __syncwarp();
+}
+
 template <int BITS>
 __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams P) {
   constexpr int RB = D * BITS / 8;
@@ -277,15 +438,15 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
   uint32_t* s_hid = reinterpret_cast<uint32_t*>(smem + OFF_HID);
   float* s_svm = reinterpret_cast<float*>(smem + OFF_SVM);
   TileBars& bar = *reinterpret_cast<TileBars*>(smem + OFF_BARS);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t spin = P.spin_limit;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.k_full[i], 4);
       mbar_init(&bar.v_full[i], 4);
-      mbar_init(&bar.k_free[i], 1);
-      mbar_init(&bar.v_free[i], 1);
+      mbar_init(&bar.k_free[i], 2);
+      mbar_init(&bar.v_free[i], 2);
       mbar_init(&bar.q_full[i], 4);
       for (int b = 0; b < 2; ++b) {
         mbar_init(&bar.s_full[i][b], 1);
@@ -296,10 +457,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
     for (int i = 0; i < 4; ++i) mbar_init(&bar.sc_full[i], 4);
     mbar_init(&bar.parts, 8);
     mbar_init(&bar.joined, 1);
-    mbar_init(&bar.drain, 1);
+    mbar_init(&bar.drain, 2);
     for (int i = 0; i < UNITS; ++i) {
       mbar_init(&bar.u_full[i], 1);
-      mbar_init(&bar.u_free[i], 13);
+      mbar_init(&bar.u_free[i], 14);
     }
     fence_mbar_init();
   }
@@ -317,12 +478,14 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
   // registers, of the 512 x 128 that the block is launched with: 128 x (2 x 152 + 104 + 104)
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(152));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(BITS == 4 ? 176 : 168));
     const int hf = warp >> 2, quarter = warp & 3;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const uint32_t t_s0 = lane_base + hf * 128, t_o = lane_base + 256 + hf * 128;
-    const int r = 32 * quarter + lane;     // row within the half
-    int tiles = 0, mine = 0, splits = 0;   // tiles seen by the CTA, steps of this half; joins
+    const int r = 32 * quarter + lane;     // row within the half (a thread per row before and after the tiles)
+    const int g = lane >> 2, t = lane & 3;
+    int tiles = 0, splits = 0;             // tiles seen by the CTA; joins
+    uint32_t par_s = 0, par_o = 0;         // bit b: parities that come next, s_full[b] and o_full[b]
     const bool special = P.cap > 0.f || P.slopes != nullptr;
     for (int k = 0; ok; ++k) {
       ok = __all_sync(0xffffffffu, mbar_wait(&bar.u_full[k % UNITS], (k / UNITS) & 1, spin));
@@ -332,11 +495,13 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
       if (rows == 0) break;
       const bool active = hf * HALF < rows;
       const int row = hf * HALF + r;
-      float f = 1.f, m = -INFINITY, l = 0.f, svr = 0.f, mneg = 0.f;
+      // the rows of this thread's fragments: 16 bk + 8 i + g at index 2 bk + i
+      float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, l[4] = {0.f, 0.f, 0.f, 0.f};
+      float svr = 0.f;
       bool far = true;
       if (active) {
         const int at = u.base + min(row, rows - 1), tok = at / P.G, head = u.h * P.G + at - tok * P.G;
-        int qpos = u.pos0 + tok;
+        int row_pos = u.pos0 + tok;
         if (P.shared) {
           // the packed token's own sequence
           int lo = 0, hi = P.batch.B;
@@ -348,9 +513,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
               hi = mid;
           }
           const Seq s = load_seq(P, lo, false);
-          qpos = s.keys ? s.pos0 + tok - s.row0 : -1;
+          row_pos = s.keys ? s.pos0 + tok - s.row0 : -1;
         }
-        const float slope = P.slopes ? P.slopes[head] * kLog2e : 0.f;
+        const float row_slope = P.slopes ? P.slopes[head] * kLog2e : 0.f;
         // this row's query, scaled by a power of two, in fp16
         const uint4* src = reinterpret_cast<const uint4*>(P.q + (u.row0 + tok) * P.sq + head * D);
         uint4 qw[16];
@@ -368,11 +533,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
         const int ex = static_cast<int>((__float_as_uint(mx) >> 23) & 0xFFu) - 127;
         const int up = mx > 0.f ? max(-126, min(126, 14 - ex)) : 0;
         float qf = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-        f = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * P.scale *
-            (P.cap > 0.f ? 1.0f / P.cap : kLog2e);
+        float row_f = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * P.scale *
+                      (P.cap > 0.f ? 1.0f / P.cap : kLog2e);
         // f >= 0 lets the maximum be taken before it is applied
-        if (f < 0.f) f = -f, qf = -qf;
-        if (f == 0.f) f = 1.f, qf = 0.f;
+        if (row_f < 0.f) row_f = -row_f, qf = -qf;
+        if (row_f == 0.f) row_f = 1.f, qf = 0.f;
         uint8_t* dst = smem + OFF_Q + hf * 2 * PANEL + r * 128;
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
@@ -392,175 +557,224 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.q_full[hf]);
-        const float ff = special ? 1.0f : f;
+        float f[4], slope[4], mneg[4];
+        int qpos[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          f[x] = __shfl_sync(0xffffffffu, row_f, 8 * x + g);
+          slope[x] = -__shfl_sync(0xffffffffu, row_slope, 8 * x + g);
+          qpos[x] = __shfl_sync(0xffffffffu, row_pos, 8 * x + g);
+          mneg[x] = 0.f;
+        }
+        float ff[4];                         // the scores' factor inside the exponential
+#pragma unroll
+        for (int x = 0; x < 4; ++x) ff[x] = special ? 1.0f : f[x];
 
-        for (int j = 0; j < steps; ++j, ++mine) {
-          const int tile = tiles + (j >> 1), ring = tile & 3, key0 = (j & 1) * (KT / 2), buf = mine & 1;
+        for (int j = 0; j < steps; ++j) {
+          const int tile = tiles + (j >> 1), ring = tile & 3, b = j & 1, key0 = b * (KT / 2);
           // scores first: they tell that every producer warp has come past the ring's last round, so
           // that a half which skipped units cannot take an older phase of the same parity for this one
-          ok = mbar_wait(&bar.s_full[hf][buf], (mine >> 1) & 1, spin);
-          if (ok && key0 == 0) ok = mbar_wait(&bar.sc_full[ring], (tile >> 2) & 1, spin);
+          ok = mbar_wait(&bar.s_full[hf][b], (par_s >> b) & 1, spin);
+          if (b == 0) ok = ok && mbar_wait(&bar.sc_full[ring], (tile >> 2) & 1, spin);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
+          par_s ^= 1u << b;
           tc_fence_after();
-          const uint32_t t_s = t_s0 + buf * (KT / 2);
-          const float4* sk4 = reinterpret_cast<const float4*>(s_sk + ring * KT + key0);
-          const float4* sv4 = reinterpret_cast<const float4*>(s_sv + ring * KT + key0);
-          const int rel = qpos - tile_pos(P, u, j >> 1) - key0;          // distance to the step's first key
-          if (special) {
-            // capped or sloped scores, in log2 units, back to tensor memory
+          const uint32_t t_s = t_s0 + key0;
+          // this lane's pairs of scales: keys 8 c + 2 t, + 1
+          const float2* sk2 = reinterpret_cast<const float2*>(s_sk + ring * KT + key0) + t;
+          const float2* sv2 = reinterpret_cast<const float2*>(s_sv + ring * KT + key0) + t;
+          const int kpos = tile_pos(P, u, j >> 1) + key0;
+          if (P.cap > 0.f) {
+            // capped scores, in log2 units, back to tensor memory
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t v[16];
-              tmem_ld16(t_s + 16 * c, v);
+            for (int c = 0; c < 8; ++c) {
+              uint32_t w[2][4];
+              const float2 sk = sk2[4 * c];
+#pragma unroll
+              for (int bk = 0; bk < 2; ++bk) tmem_ld_16x256b_x1(t_s + (bk << 20) + 8 * c, w[bk]);
               tmem_ld_wait();
-              const float d0 = static_cast<float>(rel - 16 * c);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 s = sk4[4 * c + e];
-                const float sk[4] = {s.x, s.y, s.z, s.w};
+              for (int bk = 0; bk < 2; ++bk) {
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                  float y = __uint_as_float(v[4 * e + d]) * sk[d] * f;
-                  if (P.cap > 0.f) y = P.cap * kLog2e * tanh_score(y);
-                  v[4 * e + d] = __float_as_uint(fmaf(-slope, d0 - static_cast<float>(4 * e + d), y));
-                }
+                for (int e = 0; e < 4; ++e)
+                  w[bk][e] = __float_as_uint(
+                      P.cap * kLog2e *
+                      tanh_score(__uint_as_float(w[bk][e]) * ((e & 1) ? sk.y : sk.x) * f[2 * bk + (e >> 1)]));
+                tmem_st_16x256b_x1(t_s + (bk << 20) + 8 * c, w[bk]);
               }
-              tmem_st16(t_s + 16 * c, v);
             }
             tmem_st_wait();
           }
-          // ---- 64 scores (times the key's scale; the row's factor follows), hidden ones -inf; the
-          // common case is compiled by itself: branches inside cost it half its rate
+          // ---- 64 scores (times the key's scale; the row's factor follows), hidden ones -inf
           uint32_t v[2][32];
-          tmem_ld32(t_s, v[0]);
-          tmem_ld32(t_s + 32, v[1]);
-          // keys lo .. hi - 1 of the step are visible to this row by position
-          const int hi = rel + 1, lo = P.window > 0 ? hi - P.window : 0;
+          tmem_ld_16x256b_x8(t_s, v[0]);
+          tmem_ld_16x256b_x8(t_s + (16u << 16), v[1]);
           const uint32_t flags = s_hid[ring * 8 + 4] | s_hid[ring * 8 + 5] | s_hid[ring * 8 + 6] |
                                  s_hid[ring * 8 + 7];
-          const bool general = special || __any_sync(0xffffffffu, hi < KT / 2 || lo > 0 || flags != 0u);
+          bool edge = flags != 0u;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            edge |= qpos[x] - kpos < KT / 2 - 1 || (P.window > 0 && qpos[x] - kpos >= P.window);
+          edge = __any_sync(0xffffffffu, edge);
           tmem_ld_wait();
-          auto scale = [&]() {
+          if (P.cap <= 0.f) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < 8; ++c) {
+              const float2 sk = sk2[4 * c];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 s = sk4[8 * c + e];
-                mul2u(v[c][4 * e], v[c][4 * e + 1], s.x, s.y);
-                mul2u(v[c][4 * e + 2], v[c][4 * e + 3], s.z, s.w);
+              for (int x = 0; x < 4; ++x)
+                mul2u(v[x >> 1][4 * c + 2 * (x & 1)], v[x >> 1][4 * c + 2 * (x & 1) + 1], sk.x, sk.y);
+            }
+          }
+          if (P.slopes != nullptr) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float d0 = static_cast<float>(qpos[x] - kpos - 2 * t), fx = P.cap > 0.f ? 1.0f : f[x];
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                uint32_t* w = &v[x >> 1][4 * c + 2 * (x & 1)];
+                const f2 dist = add2(f2{d0, d0}, f2{-8.0f * c, -8.0f * c - 1.0f});
+                const f2 y = fma2(f2{slope[x], slope[x]}, dist,
+                                  mul2(f2{__uint_as_float(w[0]), __uint_as_float(w[1])}, f2{fx, fx}));
+                w[0] = __float_as_uint(y.x);
+                w[1] = __float_as_uint(y.y);
               }
-          };
-          if (!special) scale();
-          if (general) {
+            }
+          }
+          if (edge) {
+            // keys lo .. hi - 1 of the step are visible to a row by position
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t seen = bits_below(hi - 32 * c) & ~bits_below(lo - 32 * c) &
-                                    ~s_hid[ring * 8 + (key0 >> 5) + c];
+            for (int x = 0; x < 4; ++x) {
+              const int hi = qpos[x] - kpos + 1, lo = P.window > 0 ? hi - P.window : 0;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[c][e] = (seen & (1u << e)) ? v[c][e] : 0xFF800000u;
+              for (int w = 0; w < 2; ++w) {
+                const uint32_t seen = (bits_below(hi - 32 * w) & ~bits_below(lo - 32 * w) &
+                                       ~s_hid[ring * 8 + (key0 >> 5) + w]) >> (2 * t);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    uint32_t& y = v[x >> 1][16 * w + 4 * c + 2 * (x & 1) + e];
+                    y = (seen & (1u << (8 * c + e))) ? y : 0xFF800000u;
+                  }
+              }
             }
           }
           // ---- references, and the sums rescaled where one has moved far
-          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          bool raise = false;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
+          for (int x = 0; x < 4; ++x) {
 #pragma unroll
-            for (int d = 0; d < 4; ++d)
-              mx4[d] = fmaxf(mx4[d], fmaxf(__uint_as_float(v[d >> 1][16 * (d & 1) + 2 * e]),
-                                           __uint_as_float(v[d >> 1][16 * (d & 1) + 2 * e + 1])));
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * ff;
+            for (int c = 0; c < 8; ++c)
+              mx[x] = fmaxf(mx[x], fmaxf(__uint_as_float(v[x >> 1][4 * c + 2 * (x & 1)]),
+                                         __uint_as_float(v[x >> 1][4 * c + 2 * (x & 1) + 1])));
+            mx[x] *= ff[x];
+            raise |= mx[x] > m[x] + (kTop + kSlack);
+          }
           const float4 sm4 = *reinterpret_cast<const float4*>(s_svm + ring * 4);
           const float svmax = fmaxf(fmaxf(sm4.x, sm4.y), fmaxf(sm4.z, sm4.w));
-          const bool raise = mx > m + 15.0f || svmax > svr;
+          raise |= svmax > svr;
           if (__any_sync(0xffffffffu, raise)) {
-            const int e2 = max(1, min(253, static_cast<int>(__float_as_uint(svmax) >> 23) + 1));
+            // a power of two above svmax
+            const int e2 = max(1, min(253, static_cast<int>(__float_as_uint(svmax) >> 23) + 2));
             const float nsv = fmaxf(svr, __uint_as_float(static_cast<uint32_t>(e2) << 23));
             const float down = svr > 0.f ? svr / nsv : 0.f;
             svr = nsv;
-            const float nm = fmaxf(m, mx - 14.0f);
-            const float fa = m == -INFINITY ? 0.f : ex2(m - nm);
-            m = nm;
-            l *= fa;
             // exp2(s - m) / svr is one exponential while both its factors are far from float32's
             // ends; otherwise 1 / svr is applied by itself
             far = svr > 1.1529215e18f || svr < 8.6736174e-19f;          // 2^60, 2^-60
-            mneg = m == -INFINITY ? 0.f : -m;
-            if (!far) mneg -= static_cast<float>(static_cast<int>(__float_as_uint(svr) >> 23) - 127);
+            float g4[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              float top = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+              const float nm = fmaxf(m[x], top - kTop);
+              const float fa = m[x] == -INFINITY ? 0.f : ex2(m[x] - nm);
+              m[x] = nm;
+              l[x] *= fa;
+              g4[x] = fa * down;
+              mneg[x] = nm == -INFINITY ? 0.f : -nm;
+              if (!far) mneg[x] -= static_cast<float>(static_cast<int>(__float_as_uint(svr) >> 23) - 127);
+            }
             if (j > 0) {
-              ok = __all_sync(0xffffffffu, mbar_wait(&bar.o_full[hf][(mine - 1) & 1], ((mine - 1) >> 1) & 1, spin));
+              // the product of the step before; its barrier's phase before that was done when these
+              // scores came
+              ok = __all_sync(0xffffffffu, mbar_wait(&bar.o_full[hf][1 - b], ((par_o >> (1 - b)) & 1) ^ 1, spin));
               if (!ok) break;
               tc_fence_after();
-              const float g = fa * down;
 #pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
-                uint32_t w[16];
-                tmem_ld16(t_o + 16 * c, w);
+              for (int c = 0; c < 4; ++c) {
+                uint32_t w[2][16];
+#pragma unroll
+                for (int bk = 0; bk < 2; ++bk) tmem_ld_16x256b_x4(t_o + (bk << 20) + 32 * c, w[bk]);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * g);
-                tmem_st16(t_o + 16 * c, w);
+                for (int bk = 0; bk < 2; ++bk) {
+#pragma unroll
+                  for (int e = 0; e < 16; ++e)
+                    w[bk][e] = __float_as_uint(__uint_as_float(w[bk][e]) * g4[2 * bk + ((e >> 1) & 1)]);
+                  tmem_st_16x256b_x4(t_o + (bk << 20) + 32 * c, w[bk]);
+                }
               }
               tmem_st_wait();
             }
           }
           // ---- weights
-          const f2 f2f{ff, ff}, f2m{mneg, mneg};
-          f2 sum{0.f, 0.f};
+          f2 sum[4] = {f2{0.f, 0.f}, f2{0.f, 0.f}, f2{0.f, 0.f}, f2{0.f, 0.f}};
+          uint32_t o[2][16];
+          // (the common case is compiled by itself: branches inside cost it half its rate)
           auto weights = [&](auto careful) {
+            const float svi = !far ? 1.0f : svr > 0.f ? 1.0f / svr : 0.f;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < 8; ++c) {
+              const float2 sv = sv2[4 * c];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                f2 a = fma2(f2{__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1])}, f2f, f2m);
+              for (int x = 0; x < 4; ++x) {
+                const int at = 4 * c + 2 * (x & 1);
+                f2 a = fma2(f2{__uint_as_float(v[x >> 1][at]), __uint_as_float(v[x >> 1][at + 1])},
+                            f2{ff[x], ff[x]}, f2{mneg[x], mneg[x]});
                 a = f2{ex2(a.x), ex2(a.y)};
-                sum = add2(sum, a);
-                v[c][2 * e] = __float_as_uint(a.x);
-                v[c][2 * e + 1] = __float_as_uint(a.y);
-              }
-              uint32_t some = 0xffffffffu;
-              if (careful.value) {           // a hidden key's scale may be infinite or NaN
-                some = 0;
-                const float svi = !far ? 1.0f : svr > 0.f ? 1.0f / svr : 0.f;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  some |= (__uint_as_float(v[c][e]) == 0.f ? 0u : 1u) << e;
-                  v[c][e] = __float_as_uint(__uint_as_float(v[c][e]) * svi);
+                sum[x] = add2(sum[x], a);
+                f2 w = careful.value ? mul2(mul2(a, f2{svi, svi}), f2{sv.x, sv.y}) : mul2(a, f2{sv.x, sv.y});
+                if (careful.value) {         // a hidden key's scale may be infinite or NaN
+                  w.x = a.x == 0.f ? 0.f : w.x;
+                  w.y = a.y == 0.f ? 0.f : w.y;
                 }
+                o[x >> 1][2 * c + (x & 1)] = h2_bits(__floats2half2_rn(w.x, w.y));
               }
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 s = sv4[8 * c + e];
-                mul2u(v[c][4 * e], v[c][4 * e + 1], s.x, s.y);
-                mul2u(v[c][4 * e + 2], v[c][4 * e + 3], s.z, s.w);
-              }
-              if (careful.value) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[c][e] = (some & (1u << e)) ? v[c][e] : 0u;
-              }
-              uint32_t o[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                o[e] = h2_bits(__floats2half2_rn(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1])));
-              tmem_st16(t_s + 16 * c, o);
             }
           };
           if (!far && !(flags & 2u))
             weights(std::false_type());
           else
             weights(std::true_type());
-          l += (sum.x + sum.y) * (far ? 1.0f : svr);
+#pragma unroll
+          for (int bk = 0; bk < 2; ++bk) tmem_st_16x128b_x8(t_s + (bk << 20), o[bk]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) l[x] += (sum[x].x + sum[x].y) * (far ? 1.0f : svr);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.p_full[hf][buf]);
+          if (lane == 0) mbar_arrive(&bar.p_full[hf][b]);
+          par_o ^= 1u << b;
         }
-        // one barrier per buffer: the product two steps back, the last one on the same barrier, is done
-        // once the scores after it are there
+        // the last product: its barrier's phase before was done when the last scores came
         if (ok && n > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&bar.o_full[hf][(mine - 1) & 1], ((mine - 1) >> 1) & 1, spin));
+          const int b = (steps - 1) & 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(&bar.o_full[hf][b], ((par_o >> b) & 1) ^ 1, spin));
           tc_fence_after();
         }
+      }
+      // a thread per row again
+      float lr = 0.f, mr = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+        const float a = __shfl_sync(0xffffffffu, l[x], 4 * (lane & 7)), c = __shfl_sync(0xffffffffu, m[x], 4 * (lane & 7));
+        if (lane >> 3 == x) lr = a, mr = c;
       }
       tiles += n;
       if (!ok) break;
@@ -574,19 +788,19 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
         const int64_t to = static_cast<int64_t>(u.piece) * P.batch.T * P.hq + out_row;
         part_o = P.ex_o + to * D;
         if (active && live) {
-          P.ex_ml[2 * to] = m;
-          P.ex_ml[2 * to + 1] = l;
+          P.ex_ml[2 * to] = mr;
+          P.ex_ml[2 * to + 1] = lr;
         }
       } else if (split) {
         float* p = P.tpart + (static_cast<int64_t>(slot) * P.nsplit + u.piece) * (2 * HALF * (D + 2));
         part_o = p + row * D;
         if (active) {
-          p[2 * HALF * D + 2 * row] = live ? m : -INFINITY;
-          p[2 * HALF * D + 2 * row + 1] = live ? l : 0.f;
+          p[2 * HALF * D + 2 * row] = live ? mr : -INFINITY;
+          p[2 * HALF * D + 2 * row + 1] = live ? lr : 0.f;
         }
       }
       if (active) {
-        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        const float inv = lr == 0.f ? 0.f : 1.0f / lr;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
@@ -600,7 +814,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
 #pragma unroll
             for (int d = 0; d < 8; ++d) {
               const float o = __uint_as_float(v[8 * c8 + place8<BITS>(d)]);
-              y[d] = n > 0 && l != 0.f ? o * svr : 0.f;
+              y[d] = n > 0 && lr != 0.f ? o * svr : 0.f;
             }
             if (part_o) {
               float4* dst = reinterpret_cast<float4*>(part_o + 32 * c + 8 * c8);
@@ -620,7 +834,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           __syncwarp();
         }
         if (!part_o && live && P.lse)
-          P.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+          P.lse[out_row] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2;
       }
       if (split) {
         // mbarriers rather than a named barrier: a half that gave up must not leave the other
@@ -700,7 +914,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
     }
   } else if (warp < 12) {
     // ----------------------------------------------------------- widening
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(104));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(BITS == 4 ? 80 : 104));
     const int pw = warp - 8, t = lane & 3, b3 = lane >> 2;
     // rows of a warp's load instruction; the two rows of a store phase differ in a bit that the
     // lanes' chunks do not use (see widen_rows)
@@ -714,10 +928,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
       if (u.rows == 0) break;
       const int n = u.n, h = u.h;
       TileCodes<BITS> kc, vc;
-      int kz[4], vz[4];
-      float sc[4];                         // lane t = 0: key scale; t = 1: value scale
-      uint32_t hidden = 0;
-      int64_t grp[4];                      // cache rows of the tile being loaded (-1: hidden)
+      // of this lane's row, wrow + lane: scales, zero points
+      float sk = 0.f, sv = 0.f;
+      int kz = 0, vz = 0;
+      bool gone = true;
+      int64_t grp[2];                      // cache rows of the warp's two groups of 16 in the tile being loaded
       auto pages = [&](int i, int (&pg)[2]) {
         const TileAt at = tile_at(P, u, min(i, n - 1));
 #pragma unroll
@@ -730,40 +945,32 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           }
         }
       };
+      // every address lies in a page: rows behind the last one are read and hidden, a group without a
+      // page reads page 0
       auto load_k = [&](int i, const int (&pg)[2]) {
         const TileAt at = tile_at(P, u, i);
-        hidden = 0;
+        const int l0 = at.local + wrow, in_page = (1 << P.pages.lps) - 1;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) grp[j] = group_of(P.pages, max(pg[j], 0), h, (l0 + 16 * j) & in_page);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int l = at.local + wrow + 8 * j + rsub;
-          const int page = pg[j >> 1];
-          const bool gone = page < 0 || l >= at.limit;
-          grp[j] = gone ? -1 : group_of(P.pages, page, h, l & ((1 << P.pages.lps) - 1));
-          hidden |= static_cast<uint32_t>(gone) << (8 * j + rsub);
-          sc[j] = 0.f;
-          kz[j] = vz[j] = 0;
+          const uint4* src = reinterpret_cast<const uint4*>(P.pages.kc + (grp[j >> 1] + 8 * (j & 1) + rsub) * RB) + t;
 #pragma unroll
-          for (int c = 0; c < BITS / 4; ++c) kc.c[j][c] = make_uint4(0u, 0u, 0u, 0u);
-          if (!gone) {
-            const uint4* src = reinterpret_cast<const uint4*>(P.pages.kc + grp[j] * RB) + t;
-#pragma unroll
-            for (int c = 0; c < BITS / 4; ++c) kc.c[j][c] = __ldg(src + 4 * c);
-            kz[j] = __ldg(P.pages.kz + grp[j]);
-            vz[j] = __ldg(P.pages.vz + grp[j]);
-            if (t < 2) sc[j] = __ldg((t ? P.pages.vs : P.pages.ks) + grp[j]);
-          }
+          for (int c = 0; c < BITS / 4; ++c) kc.c[j][c] = __ldg(src + 4 * c);
         }
+        const int64_t mine = (lane < 16 ? grp[0] : grp[1]) + (lane & 15);
+        sk = __ldg(P.pages.ks + mine);
+        sv = __ldg(P.pages.vs + mine);
+        kz = __ldg(P.pages.kz + mine);
+        vz = __ldg(P.pages.vz + mine);
+        gone = (lane < 16 ? pg[0] : pg[1]) < 0 || l0 + lane >= at.limit;
       };
       auto load_v = [&]() {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+          const uint4* src = reinterpret_cast<const uint4*>(P.pages.vc + (grp[j >> 1] + 8 * (j & 1) + rsub) * RB) + t;
 #pragma unroll
-          for (int c = 0; c < BITS / 4; ++c) vc.c[j][c] = make_uint4(0u, 0u, 0u, 0u);
-          if (grp[j] >= 0) {
-            const uint4* src = reinterpret_cast<const uint4*>(P.pages.vc + grp[j] * RB) + t;
-#pragma unroll
-            for (int c = 0; c < BITS / 4; ++c) vc.c[j][c] = __ldg(src + 4 * c);
-          }
+          for (int c = 0; c < BITS / 4; ++c) vc.c[j][c] = __ldg(src + 4 * c);
         }
       };
       int pg[2];
@@ -778,34 +985,22 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
         const uint32_t par = ((tiles >> 1) & 1) ^ 1;   // a fresh barrier counts as free
         ok = __all_sync(0xffffffffu, mbar_wait(&bar.k_free[st], par, spin));
         if (!ok) break;
-        int vz_now[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) vz_now[j] = vz[j];
+        const int vz_now = vz;
         widen_rows<BITS>(smem + OFF_K + st * 2 * PANEL, kc, kz, wrow, rsub, t);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.k_full[st]);
         // scales, hidden keys
-        float svm = 0.f;
-        bool bad = false;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int row = wrow + 8 * j + rsub;
-          if (t == 0) s_sk[ring * KT + row] = sc[j];
-          if (t == 1) {
-            s_sv[ring * KT + row] = sc[j];
-            const float a = fabsf(sc[j]);
-            svm = fmaxf(svm, a <= 3.0e38f ? a : 0.f);
-            bad |= !(a <= 3.0e38f);
-          }
-        }
-        svm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(svm)));
-        const uint32_t hid = __reduce_or_sync(0xffffffffu, hidden);
-        const bool any_bad = __any_sync(0xffffffffu, bad);
+        s_sk[ring * KT + wrow + lane] = sk;
+        s_sv[ring * KT + wrow + lane] = gone ? 0.f : sv;
+        const float a = gone ? 0.f : fabsf(sv);
+        const bool fine = a <= 3.0e38f;
+        const uint32_t svm = __reduce_max_sync(0xffffffffu, fine ? __float_as_uint(a) : 0u);
+        const uint32_t hid = __ballot_sync(0xffffffffu, gone), bad = __ballot_sync(0xffffffffu, !fine);
         if (lane == 0) {
-          s_svm[ring * 4 + pw] = svm;
+          s_svm[ring * 4 + pw] = __uint_as_float(svm);
           s_hid[ring * 8 + pw] = hid;
-          s_hid[ring * 8 + 4 + pw] = (hid != 0 ? 1u : 0u) | (any_bad ? 2u : 0u);
+          s_hid[ring * 8 + 4 + pw] = (hid != 0 ? 1u : 0u) | (bad != 0 ? 2u : 0u);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.sc_full[ring]);
@@ -826,90 +1021,14 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
     }
   } else {
     // ------------------------------------------------------------ products
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(BITS == 4 ? 80 : 72));
+    // one warp per half, which sleeps while its half has nothing to do: a single one that polls both
+    // halves' barriers takes issue slots and shared memory from the warps that work
     if (warp == 12) {
-    int tiles = 0, qs = 0, cnt = 0;          // qs: bit h, half h's parity; cnt: 2 bits, its steps so far
-    const uint64_t q_desc = desc_sw128(smem_u32(smem + OFF_Q)), k_desc = desc_sw128(smem_u32(smem + OFF_K)),
-                   v_desc = desc_sw128_mn(smem_u32(smem + OFF_V), PANEL, 1024);
-    for (int k = 0; ok; ++k) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&bar.u_full[k % UNITS], (k / UNITS) & 1, spin));
-      if (!ok) break;
-      const volatile TileUnit& u = ring_u[k % UNITS];
-      const int rows = u.rows, n = u.n, steps = u.steps;
-      if (rows == 0) break;
-      const int halves = rows > HALF ? 2 : 1;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.u_free[k % UNITS]);
-      // descriptors advance by constants in their low word (addresses / 16): few registers
-      auto scores = [&](int h, int j, int buf) {
-        if (lane == 0) {
-          const int stage = (tiles + (j >> 1)) & 1;
-          const uint64_t a = q_desc + ((h * 2 * PANEL) >> 4),
-                         b = k_desc + ((stage * 2 * PANEL + (j & 1) * (PANEL / 2)) >> 4);
-#pragma unroll
-          for (int s = 0; s < 8; ++s) {
-            const uint32_t off = ((s >> 2) * PANEL + (s & 3) * 32) >> 4;
-            mma_f16_ss(tmem + h * 128 + buf * (KT / 2), a + off, b + off, IDESC_S, s > 0);
-          }
-          mma_commit(&bar.s_full[h][buf]);
-          if (h == halves - 1 && ((j & 1) || j == steps - 1)) mma_commit(&bar.k_free[stage]);
-        }
-        __syncwarp();
-      };
-      for (int h = 0; h < halves && ok; ++h) {
-        ok = mbar_wait(&bar.q_full[h], (qs >> h) & 1, spin);
-        qs ^= 1 << h;
-      }
-      if (ok && n > 0) ok = mbar_wait(&bar.k_full[tiles & 1], (tiles >> 1) & 1, spin);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      // two steps of scores ahead: a half's next scores are there when its softmax ends
-#pragma unroll 1
-      for (int j = 0; j < min(steps, 2); ++j)
-#pragma unroll 1
-        for (int h = 0; h < halves; ++h) scores(h, j, ((cnt >> (2 * h)) + j) & 1);
-      for (int j = 0; j < steps && ok; ++j) {
-        const int tile = tiles + (j >> 1);
-#pragma unroll 1
-        for (int h = 0; h < halves && ok; ++h) {
-          const int c = (cnt >> (2 * h)) & 3, buf = c & 1;
-          ok = mbar_wait(&bar.p_full[h][buf], c >> 1, spin);
-          cnt = (cnt & ~(3 << (2 * h))) | (((c + 1) & 3) << (2 * h));
-          if (ok && h == 0 && !(j & 1)) ok = mbar_wait(&bar.v_full[tile & 1], (tile >> 1) & 1, spin);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint64_t b = v_desc + (((tile & 1) * 2 * PANEL + (j & 1) * (PANEL / 2)) >> 4);
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-              mma_f16_ts(tmem + 256 + h * 128, tmem + h * 128 + buf * (KT / 2) + 8 * s, b + s * (2048 >> 4),
-                         IDESC_O, j > 0 || s > 0);
-            mma_commit(&bar.o_full[h][buf]);
-            if (h == halves - 1 && ((j & 1) || j == steps - 1)) mma_commit(&bar.v_free[tile & 1]);
-          }
-          __syncwarp();
-          if (j + 2 < steps) {
-            if (h == 0 && !(j & 1)) {
-              ok = __all_sync(0xffffffffu,
-                              mbar_wait(&bar.k_full[(tile + 1) & 1], ((tile + 1) >> 1) & 1, spin));
-              if (!ok) break;
-              tc_fence_after();
-            }
-            scores(h, j + 2, buf);
-          }
-        }
-      }
-      tiles += n;
-    }
-    // no product may still write the tensor memory freed below
-    if (lane == 0) {
-      mma_commit(&bar.drain);
-      mbar_wait(&bar.drain, 0, 0);
-    }
-    __syncwarp();
+      issue_products<0>(P, smem, bar, ring_u);
     } else if (warp == 13) {
+      issue_products<1>(P, smem, bar, ring_u);
+    } else if (warp == 14) {
       // ------------------------------------------------------------- units
       const int64_t units = P.units;
       int at = 0;

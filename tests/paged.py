@@ -94,7 +94,7 @@ class Attention:
             size = max(size, z)
         return out, lse, spread, size
 
-    def bounds(self, ref, weight_eps):
+    def bounds(self, ref, weight_eps, weight_step=2.0 ** -37):
         """Elementwise bounds of out and lse.
 
         A score's error: its exact products are summed in float32 in 8 steps of 16, each sum off by at
@@ -107,11 +107,14 @@ class Attention:
         Weights (times the value's scale) far below a row's largest are held in fixed steps: half a step
         of fp16's smallest, 2^-25, where the largest weight is 2^14 or more and the scales are measured in
         a power of two at most four times the largest: each key adds 2^-25 2^-14 4 top, with top the
-        largest scale times code, at most the range of the codes times the scale."""
+        largest scale times code, at most the range of the codes times the scale.  That is 2^-37, the
+        streaming kernel's `weight_step`; where the largest weight is 2^10 or more and the scales are
+        measured in a power of two at most eight times the largest (the tile kernel) it is
+        2^-25 2^-10 8 = 2^-32."""
         out, lse, spread, size = ref
         e = 2.0 ** -18 * (1 + size) + self.rule["softcap"] * 2.0 ** -20
         top = max(float(np.abs(v).max()) if v.size else 0.0 for (k, _), v in self.values.items() if k == "v")
         top *= 2                                     # an asymmetric grid's other end is no further than its range
-        step = (self.prefix + max(self.own, default=0)) * 2.0 ** -37 * top
+        step = (self.prefix + max(self.own, default=0)) * weight_step * top
         return (2.0 ** -8 * np.abs(out) + 2 * (e + weight_eps) * spread + step + 1e-30,
                 e + 2.0 ** -20 * (1 + np.abs(np.where(np.isfinite(lse), lse, 0.0))))

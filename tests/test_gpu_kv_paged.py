@@ -14,6 +14,7 @@ D = 128
 STREAM_EPS = 2.0 ** -19      # weights held as two fp16 halves (2^-22) and ex2 (2^-22), sums of both
 # the tile kernel holds weights (times the value's scale) in one fp16 number: half a step is 2^-11 of it
 TILE_EPS = 2.0 ** -11 + STREAM_EPS
+TILE_STEP = 2.0 ** -32
 
 
 def cu(a, dtype=None):
@@ -55,7 +56,7 @@ def weight_eps(prob):
 def check(prob, out, lse):
     ref = prob.reference()
     eps = weight_eps(prob)
-    b_out, b_lse = prob.bounds(ref, eps)
+    b_out, b_lse = prob.bounds(ref, eps, *([TILE_STEP] if eps == TILE_EPS else []))
     o, m = out.double().cpu().numpy(), lse.double().cpu().numpy()
     n = sum(prob.new)
     assert (o[n:] == 7).all() and (m[n:] == 7).all(), "rows behind the last sequence were written"
@@ -320,7 +321,7 @@ def test_many_rows_hidden_infinities_do_not_leak():
         for key in "kv":
             getattr(pages, key + "_scale")[page, :, row] = bad if key in keys else 0.5
         out, lse = attend(prob, pages)
-        b_out, b_lse = prob.bounds(ref, TILE_EPS)
+        b_out, b_lse = prob.bounds(ref, TILE_EPS, TILE_STEP)
         o, m = out.double().cpu().numpy(), lse.double().cpu().numpy()
         assert (np.abs(o[:63] - ref[0][:63]) <= b_out[:63]).all()
         assert (np.abs(m[:63] - ref[1][:63]) <= b_lse[:63]).all()
