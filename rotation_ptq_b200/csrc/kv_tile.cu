@@ -245,6 +245,13 @@ __device__ __forceinline__ void mul2u(uint32_t& a, uint32_t& b, float x, float y
   b = __float_as_uint(r.y);
 }
 
+// The largest of three; NaN loses, as with fmaxf.
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return y;
+}
+
 // Tensor memory in the fragment layout, 16 lanes (rows) at a time.  Lane (g, t) = (lane / 4, lane % 4)
 // of the warp holds, of every group of 8 columns, columns 2t, 2t + 1 of row g (registers 4 i, 4 i + 1
 // of group i) and of row g + 8 (4 i + 2, 4 i + 3); of 16-bit pairs, every group of 4 columns, column t
@@ -566,6 +573,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           qpos[x] = __shfl_sync(0xffffffffu, row_pos, 8 * x + g);
           mneg[x] = 0.f;
         }
+        const int qmin = __reduce_min_sync(0xffffffffu, row_pos), qmax = __reduce_max_sync(0xffffffffu, row_pos);
         float ff[4];                         // the scores' factor inside the exponential
 #pragma unroll
         for (int x = 0; x < 4; ++x) ff[x] = special ? 1.0f : f[x];
@@ -610,13 +618,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           uint32_t v[2][32];
           tmem_ld_16x256b_x8(t_s, v[0]);
           tmem_ld_16x256b_x8(t_s + (16u << 16), v[1]);
-          const uint32_t flags = s_hid[ring * 8 + 4] | s_hid[ring * 8 + 5] | s_hid[ring * 8 + 6] |
-                                 s_hid[ring * 8 + 7];
-          bool edge = flags != 0u;
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            edge |= qpos[x] - kpos < KT / 2 - 1 || (P.window > 0 && qpos[x] - kpos >= P.window);
-          edge = __any_sync(0xffffffffu, edge);
+          const uint4 fl = *reinterpret_cast<const uint4*>(s_hid + ring * 8 + 4);
+          const uint32_t flags = fl.x | fl.y | fl.z | fl.w;
+          const bool edge = flags != 0u || kpos + KT / 2 - 1 > qmin || (P.window > 0 && qmax - kpos >= P.window);
           tmem_ld_wait();
           if (P.cap <= 0.f) {
 #pragma unroll
@@ -668,8 +672,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           for (int x = 0; x < 4; ++x) {
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-              mx[x] = fmaxf(mx[x], fmaxf(__uint_as_float(v[x >> 1][4 * c + 2 * (x & 1)]),
-                                         __uint_as_float(v[x >> 1][4 * c + 2 * (x & 1) + 1])));
+              mx[x] = max3(mx[x], v[x >> 1][4 * c + 2 * (x & 1)], v[x >> 1][4 * c + 2 * (x & 1) + 1]);
             mx[x] *= ff[x];
             raise |= mx[x] > m[x] + (kTop + kSlack);
           }
