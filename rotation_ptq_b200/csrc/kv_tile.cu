@@ -233,6 +233,11 @@ __device__ __forceinline__ constexpr int place8(int d) {
   return BITS == 8 ? d : (d < 4 ? 2 * d : 2 * (d - 4) + 1);
 }
 
+// Where 16-byte chunk c of a row of 256 bytes lies in two swizzled panels.
+__device__ __forceinline__ int chunk_at(int row, int c) {
+  return (c >> 3) * PANEL + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+}
+
 // Bits 0 .. n - 1, n clamped to 0 .. 32.
 __device__ __forceinline__ uint32_t bits_below(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
@@ -523,32 +528,35 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           row_pos = s.keys ? s.pos0 + tok - s.row0 : -1;
         }
         const float row_slope = P.slopes ? P.slopes[head] * kLog2e : 0.f;
-        // this row's query, scaled by a power of two, in fp16
-        const uint4* src = reinterpret_cast<const uint4*>(P.q + (u.row0 + tok) * P.sq + head * D);
+        // the warp's queries, scaled per row by a power of two, in fp16: 16 lanes a row, so that loads
+        // are of whole lines (a thread per row: 4096 sectors a unit through the L1, 3 us)
+        const int64_t row_at = static_cast<int64_t>(u.row0 + tok) * P.sq + head * D;
+        const int c16 = lane & 15;
         uint4 qw[16];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) qw[c] = __ldg(src + c);
-        float mx = 0.f;
+        for (int i = 0; i < 16; ++i)
+          qw[i] = __ldg(reinterpret_cast<const uint4*>(P.q + __shfl_sync(0xffffffffu, row_at, 2 * i + (lane >> 4))) + c16);
+        float row_f = 1.f;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const uint32_t ws[4] = {qw[c].x, qw[c].y, qw[c].z, qw[c].w};
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t ws[4] = {qw[i].x, qw[i].y, qw[i].z, qw[i].w};
+          float mx = 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(ws[e] << 16)),
                                  fabsf(__uint_as_float(ws[e] & 0xFFFF0000u))));
-        }
-        const int ex = static_cast<int>((__float_as_uint(mx) >> 23) & 0xFFu) - 127;
-        const int up = mx > 0.f ? max(-126, min(126, 14 - ex)) : 0;
-        float qf = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-        float row_f = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * P.scale *
-                      (P.cap > 0.f ? 1.0f / P.cap : kLog2e);
-        // f >= 0 lets the maximum be taken before it is applied
-        if (row_f < 0.f) row_f = -row_f, qf = -qf;
-        if (row_f == 0.f) row_f = 1.f, qf = 0.f;
-        uint8_t* dst = smem + OFF_Q + hf * 2 * PANEL + r * 128;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const uint32_t ws[4] = {qw[c].x, qw[c].y, qw[c].z, qw[c].w};
+          for (int of = 1; of < 16; of <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, of));
+          const int ex = static_cast<int>((__float_as_uint(mx) >> 23) & 0xFFu) - 127;
+          const int up = mx > 0.f ? max(-126, min(126, 14 - ex)) : 0;
+          float qf = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+          float f = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * P.scale *
+                    (P.cap > 0.f ? 1.0f / P.cap : kLog2e);
+          // a factor >= 0 lets the maximum be taken before it is applied
+          if (f < 0.f) f = -f, qf = -qf;
+          if (f == 0.f) f = 1.f, qf = 0.f;
+          const float both = __shfl_sync(0xffffffffu, f, (lane & 1) << 4);   // of row 2 i + (lane & 1)
+          if (lane >> 1 == i) row_f = both;
           float v[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -558,7 +566,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           uint32_t o[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[e] = h2_bits(__floats2half2_rn(v[2 * e], v[2 * e + 1]));
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * PANEL + (((c & 7) ^ (r & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(smem + OFF_Q + hf * 2 * PANEL + chunk_at(32 * quarter + 2 * i + (lane >> 4), c16)) =
               make_uint4(o[0], o[1], o[2], o[3]);
         }
         fence_proxy_async_smem();
@@ -786,55 +794,79 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
       const bool split = pieces > 1 && !P.shared, live = row < rows;
       const int at = u.base + min(row, rows - 1), tok = at / P.G, head = u.h * P.G + at - tok * P.G;
       const int64_t out_row = static_cast<int64_t>(u.row0 + tok) * P.hq + head;
-      float* part_o = nullptr;
+      float* part_o = nullptr;               // partial results, and this row's place in them
+      int64_t part_row = 0;
       if (P.shared) {
         const int64_t to = static_cast<int64_t>(u.piece) * P.batch.T * P.hq + out_row;
-        part_o = P.ex_o + to * D;
+        part_o = P.ex_o + static_cast<int64_t>(u.piece) * P.batch.T * P.hq * D;
+        part_row = out_row;
         if (active && live) {
           P.ex_ml[2 * to] = mr;
           P.ex_ml[2 * to + 1] = lr;
         }
       } else if (split) {
         float* p = P.tpart + (static_cast<int64_t>(slot) * P.nsplit + u.piece) * (2 * HALF * (D + 2));
-        part_o = p + row * D;
+        part_o = p;
+        part_row = row;
         if (active) {
           p[2 * HALF * D + 2 * row] = live ? mr : -INFINITY;
           p[2 * HALF * D + 2 * row + 1] = live ? lr : 0.f;
         }
       }
       if (active) {
+        // through this half's queries, which nothing reads any more, so that 16 lanes store a row's
+        // whole lines
         const float inv = lr == 0.f ? 0.f : 1.0f / lr;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          if (n > 0) {
-            tmem_ld32(t_o + 32 * c, v);
-            tmem_ld_wait();
-          }
-#pragma unroll
-          for (int c8 = 0; live && c8 < 4; ++c8) {
-            float y[8];
-#pragma unroll
-            for (int d = 0; d < 8; ++d) {
-              const float o = __uint_as_float(v[8 * c8 + place8<BITS>(d)]);
-              y[d] = n > 0 && lr != 0.f ? o * svr : 0.f;
+        uint8_t* stage = smem + OFF_Q + hf * 2 * PANEL;
+        const int lane_row = part_o ? static_cast<int>(part_row) : static_cast<int>(out_row);
+        const int passes = part_o ? 2 : 1;
+#pragma unroll 1
+        for (int pass = 0; pass < passes; ++pass) {
+          __syncwarp();
+#pragma unroll 1
+          for (int c = 2 * pass; c < (part_o ? 2 * pass + 2 : 4); ++c) {
+            uint32_t v[32];
+            if (n > 0) {
+              tmem_ld32(t_o + 32 * c, v);
+              tmem_ld_wait();
             }
-            if (part_o) {
-              float4* dst = reinterpret_cast<float4*>(part_o + 32 * c + 8 * c8);
-              dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-              dst[1] = make_float4(y[4], y[5], y[6], y[7]);
-            } else {
-              uint32_t w[4];
 #pragma unroll
-              for (int d = 0; d < 4; ++d) {
-                __nv_bfloat162 b2 = __floats2bfloat162_rn(y[2 * d] * inv, y[2 * d + 1] * inv);
-                w[d] = *reinterpret_cast<uint32_t*>(&b2);
+            for (int c8 = 0; c8 < 4; ++c8) {
+              float y[8];
+#pragma unroll
+              for (int d = 0; d < 8; ++d) {
+                const float o = __uint_as_float(v[8 * c8 + place8<BITS>(d)]);
+                y[d] = n > 0 && lr != 0.f ? o * svr : 0.f;
               }
-              *reinterpret_cast<uint4*>(P.out + out_row * D + 32 * c + 8 * c8) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
+              if (part_o) {
+                const int at = 8 * (c & 1) + 2 * c8;
+                *reinterpret_cast<float4*>(stage + chunk_at(r, at)) = make_float4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<float4*>(stage + chunk_at(r, at + 1)) = make_float4(y[4], y[5], y[6], y[7]);
+              } else {
+                uint32_t w[4];
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                  __nv_bfloat162 b2 = __floats2bfloat162_rn(y[2 * d] * inv, y[2 * d + 1] * inv);
+                  w[d] = *reinterpret_cast<uint32_t*>(&b2);
+                }
+                *reinterpret_cast<uint4*>(stage + chunk_at(r, 4 * c + c8)) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
             }
           }
           __syncwarp();
+          const int live_rows = min(32, rows - hf * HALF - 32 * quarter);
+#pragma unroll 4
+          for (int i = 0; i < 16; ++i) {
+            const int q = 2 * i + (lane >> 4);
+            const int64_t to = __shfl_sync(0xffffffffu, lane_row, q);
+            if (q < live_rows) {
+              const uint4 w = *reinterpret_cast<const uint4*>(stage + chunk_at(32 * quarter + q, lane & 15));
+              if (part_o)
+                *reinterpret_cast<uint4*>(part_o + to * D + 64 * pass + 4 * (lane & 15)) = w;
+              else
+                *reinterpret_cast<uint4*>(P.out + to * D + 8 * (lane & 15)) = w;
+            }
+          }
         }
         if (!part_o && live && P.lse)
           P.lse[out_row] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2;
