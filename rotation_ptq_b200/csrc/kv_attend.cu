@@ -869,12 +869,19 @@ int stream_grid(int bits, int kind) {
   return grid;
 }
 
-// Sequences of up to this many rows (new tokens x query heads per KV head)
-// go to the streaming kernel, longer ones to the tile kernel.
-constexpr int kFewRows = 16;
-// A shared prefix is read once for the batch while no sequence has more rows
-// than this; longer ones fill the tile kernel's rows by themselves.
+// Sequences of up to this many rows (new tokens x query heads per KV head) go to the streaming kernel
+// (in units of 16), longer ones to the tile kernel, whose 128 rows a half cost the same however few of
+// them live.  4-bit, 4000 keys, streaming against tile, us: 32 rows of 1, 4, 16 sequences 29 / 28,
+// 36 / 44, 85 / 103; 48 rows 30 / 34, 52 / 46, 122 / 102.
+constexpr int kFewRows = 32;
+// A shared prefix is read once for the batch (by the tile kernel, whose partial results the streaming
+// kernel joins) while no sequence has more rows than kSharedRows - longer ones fill the tile kernel's
+// rows by themselves - and the streaming kernel's tiles over the prefix, for each sequence anew, would
+// come to kSharedTiles an SM.  4-bit, us, streaming against shared: 16 single tokens behind 4096 keys
+// 38 / 42, behind 10000 67 / 52; 32 behind 2000 42 / 43, behind 4096 60 / 44; 64 behind 700 44 / 55,
+// behind 2000 65 / 55; 5 new tokens each, 6 sequences behind 2000 39 / 47, 32 behind 2000 108 / 89.
 constexpr int kSharedRows = 128;
+constexpr int kSharedTiles = 30;
 constexpr int kTileRows = 256;
 constexpr size_t kPartFloats = static_cast<size_t>(kTileRows) * (D + 2);
 
@@ -884,7 +891,10 @@ AttnPlan make_plan(int64_t T, int hq, int hkv, int B, int max_q, int64_t keys, i
   const int64_t G = hq / hkv, rows = G * max_q;
   const int sms = host::num_sms();
   p.kind = rows <= 4 ? 0 : rows <= 8 ? 1 : 2;
-  p.shared = prefix_len > 0 && rows <= kSharedRows && B > 1 && have_ws;
+  const int64_t per_unit = stream_of(bits, p.kind).rows;
+  p.shared = have_ws && B > 1 && prefix_len > 0 && rows <= kSharedRows &&
+             B * ((rows + per_unit - 1) / per_unit) * hkv * ((prefix_len + TILE - 1) / TILE) >=
+                 static_cast<int64_t>(kSharedTiles) * sms;
   p.tile = !p.shared && rows > kFewRows;
   p.stream = p.shared || !p.tile || B > 1;
   p.tile_split = 1;

@@ -291,6 +291,23 @@ def test_prefix_of_a_batch(prefix, batch, new, page, bits, rule):
     check(prob, *attend(prob))
 
 
+@pytest.mark.parametrize("rule", [{}, dict(softcap=20.0), dict(window=700), dict(slopes=True), dict(v_size=1e4)])
+@pytest.mark.parametrize("prefix,batch,new,hq,hkv,page,bits", [
+    (1000, 160, 1, 8, 4, 16, 4),                    # two blocks of rows per KV head
+    (1793, 40, 8, 16, 4, 64, 8),                    # five, of ragged drafts
+    (3001, 24, 17, 8, 2, 32, 4)])                   # more rows than the streaming kernel takes by itself
+def test_prefix_read_once(prefix, batch, new, hq, hkv, page, bits, rule):
+    """Batches whose prefix is long enough for a pass of its own, on any device of at least 148 SMs' worth
+    of streaming tiles (30 an SM)."""
+    own = [new + (11 * b) % 50 for b in range(batch)]
+    count = [max(0, new - b % 3) for b in range(batch)]
+    rows = new * hq // hkv
+    per = 4 if rows <= 4 else 8 if rows <= 8 else 16
+    assert batch * -(-rows // per) * hkv * -(-prefix // 128) >= 30 * 148
+    prob = G.Attention(39, count, own, hq, hkv, page, bits, prefix=prefix, pad=2, **rule)
+    check(prob, *attend(prob))
+
+
 def test_many_rows_split_and_repeat():
     prob = G.Attention(36, [40, 3], [2500, 9], 8, 2, 64, 4)
     a = attend(prob)
