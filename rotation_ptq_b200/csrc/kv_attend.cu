@@ -265,7 +265,10 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
   // equal pieces but for the last; a unit's pieces belong to consecutive CTAs
   const int64_t piece = slots ? 1 : (total + gridDim.x - 1) / gridDim.x;
   const int64_t r0 = piece * blockIdx.x, r1 = min(total, r0 + piece);
-  if (r0 >= r1) return;
+  if (r0 >= r1) {
+    griddep_wait();                        // this kernel's end tells that of the shared prefix's pass too
+    return;
+  }
   if (r0 >= excl && r0 < excl + mine) {
     int b = bfirst;
     int64_t base = excl;
@@ -802,7 +805,8 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
         row[r] = static_cast<int64_t>(u.s.row0 + tok) * P.hq + u.h * G + u.row0 + rr - tok * G;
       }
       if (P.ex_n > 0) {
-        // the shared prefix's part of the rows, in pieces
+        // the shared prefix's part of the rows, in pieces (the pass may have run beside this kernel so far)
+        griddep_wait();
         const int64_t step = P.batch.T * P.hq;
         join(P.ex_n,
              [&](int j, int r) {           // r is not known to the compiler here
@@ -985,8 +989,19 @@ sq_status run_attention(const void* q, int64_t q_stride, int64_t T, int hq,
   P.ex_n = plan.shared ? plan.tile_split : 0;
   const int grid = stream_grid(pages.bits, plan.kind);
   const StreamKernel k = stream_of(pages.bits, plan.kind);
-  k.fn<<<grid, THREADS, k.smem, stream>>>(P);
-  cudaError_t e = cudaGetLastError();
+  // behind a pass over the shared prefix: a programmatic dependent, whose CTAs begin with the sequences'
+  // own keys as that pass's end
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = k.smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = plan.shared ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k.fn, P);
   return e == cudaSuccess ? SQ_OK : host::cuda_fail("kv attention launch", e);
 }
 

@@ -453,6 +453,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t spin = P.spin_limit;
 
+  if (P.shared) griddep_launch_dependents();           // the streaming kernel that joins
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.k_full[i], 4);
