@@ -18,12 +18,13 @@
 // over a long cache of codes that are all positive would lose, against one of
 // both signs, what its mean is larger than the result.
 //
-// What bounds it: issue slots, then the cache's bytes.  A warp's step of 16
-// keys x 128 channels took 592 instructions with codes widened to whole
-// numbers and loads straight to registers (long 4-bit caches: 158 us for 280
-// MB); see the end of this file for what it takes now.  Loads go through a
-// ring of 16-key slots in shared memory per warp (cp.async, no exchange
-// between warps), D - 1 slots ahead.
+// What bounds it: issue slots, and the beginning and end of a unit (about 3 us
+// from its first load to its first key and 4 from its last key to the end of
+// its pieces' join).  16 keys x 128 channels take a warp 363 instructions
+// (592 with codes widened to whole numbers and loads straight to registers);
+// two documents of 118 to 131 thousand keys, 280 MB: 85 us (158), of which the
+// keys 60, at 4.7 TB/s.  Loads go through a ring of two slots of 32 keys in
+// shared memory per warp (cp.async, no exchange between warps).
 //
 // Exactness: queries are scaled per row by a power of two that puts the
 // largest at 2^14..2^15 and held in fp16 (a bf16 value has 8 significant
@@ -191,7 +192,7 @@ struct Stream {
 template <int BITS, int NT, bool PAIR>
 __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_kernel(const AttnParams P) {
   using St = Stream<BITS, NT, PAIR>;
-  constexpr int R = St::R, RB = St::RB, DEPTH = St::DEPTH;
+  constexpr int R = St::R, RB = St::RB;
   extern __shared__ __align__(128) uint8_t stream_smem[];
   auto sm_o = [&](int w) { return reinterpret_cast<float(*)[D]>(stream_smem + w * St::RING); };
   __shared__ float sm_m[WARPS][R], sm_l[WARPS][R], sm_f[THREADS], sm_fl[THREADS], sm_top[R];
@@ -662,7 +663,9 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
       __syncwarp();
     }
 
-    // ---- the warps' results into shared memory, at a common maximum
+    // ---- the warps' results into shared memory.  Sums that large scales might carry past float32's end
+    // before they are divided stand at 2^-40 of themselves, their reference 40 higher.
+    const float back = 16777216.0f * (svr >= 1.0f ? 9.094947e-13f : 1.0f);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -673,8 +676,8 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
           l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], of);
         }
         if (g == 0 && r < R) {
-          sm_m[warp][r] = m[n][c];
-          sm_l[warp][r] = l[n][c];
+          sm_m[warp][r] = svr >= 1.0f ? m[n][c] + 40.0f : m[n][c];
+          sm_l[warp][r] = svr >= 1.0f ? l[n][c] * 9.094947e-13f : l[n][c];
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -683,8 +686,8 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
             x += __shfl_down_sync(0xffffffffu, x, 2);
             y += __shfl_down_sync(0xffffffffu, y, 2);
           }
-          x = x * 16777216.0f * svr;
-          y = y * (BITS == 4 ? 1048576.0f : 16777216.0f) * svr;
+          x = x * back * svr;
+          y = y * (BITS == 4 ? 0.0625f * back : back) * svr;
           if (r < R) *reinterpret_cast<float2*>(&sm_o(warp)[r][16 * g + 2 * i]) = make_float2(x, y);
         }
       }

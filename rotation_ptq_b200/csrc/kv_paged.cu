@@ -115,12 +115,11 @@ __device__ __forceinline__ R scale_and_turn(const uint4 (&raw)[2], const __nv_bf
       y[e] = a * C - b * S;
       y[8 + e] = b * C + a * S;
     }
-    return sum;
   }
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int e0 = 64 * c + 8 * s;
-    if (e0 >= rot) continue;
+    if (WHOLE || e0 >= rot) continue;
     if (interleaved) {
       const float4 c4 = __ldg(reinterpret_cast<const float4*>(cs + e0 / 2));
       const float4 s4 = __ldg(reinterpret_cast<const float4*>(sn + e0 / 2));
@@ -251,7 +250,7 @@ __device__ __forceinline__ void store_quantized(const float (&y)[16], int s, uns
 
 // WHOLE: half layout over the whole head.
 template <int BITS, bool WHOLE>
-__global__ void __launch_bounds__(256) append_kernel(const AppendParams P) {
+__global__ void __launch_bounds__(256, 3) append_kernel(const AppendParams P) {
   const int lane = threadIdx.x & 31, s = lane & (LPV - 1), vec = lane / LPV;
   const unsigned mask = 0xFFu << (lane & 24);
   const int jobs = P.jq + 2 * P.jk;        // four heads each: Q, K, V

@@ -10,22 +10,31 @@
 // sv stay outside the products, so fp16 operands lose nothing; P is rounded
 // once to 11 bits, an eighth of what the bf16 output's own rounding may lose.
 //
-// Warps: 0-3 and 4-7 softmax of half 0 and 1 (in the fragment layout: a
-// lane needs the scales of a quarter of the keys.  With a thread per row every
-// lane reads them all, and those reads and the products' operands stand in one
-// another's way in shared memory: the softmax took 1.7 times as long), 8-11 widen codes from global memory into swizzled shared
-// memory, 12 and 13 issue the halves' products, 14 works out
-// the units.  A step is 64 keys and
-// each half has two buffers of scores, so that the next step's scores are there when a softmax ends;
-// the halves run independently.
+// Warps: 0-3 and 4-7 softmax of half 0 and 1, 8-11 widen codes from global
+// memory into swizzled shared memory, 12 and 13 issue the halves' products, 14
+// works out the units.  A step is 64 keys and each half has two buffers of
+// scores, so that the next step's scores are there when a softmax ends; the
+// halves run independently.
 //
-// Two rows of work: a sequence's own rows over what it sees (splits of a
+// What it took (prompts of 2 x 4096, 4 bits, us): an issuing warp whose
+// descriptors do not spill, 920 to 710; the softmax's common case without
+// branches, 566; one uniform issuing warp per half, 540 (a step's 12 products
+// took 1500 cycles to issue from inside a branch, and 500 now); references with
+// a slack, so that few steps rescale; the softmax in the fragment layout, where
+// a lane needs the scales of a quarter of the keys (with a thread per row every
+// lane reads them all: those broadcasts and the products' operand reads, both
+// from shared memory, slow one another 1.5 times).  What bounds it now is the
+// softmax's own latency: without its arithmetic the rest takes 275 us, without
+// the products' 460, without the exponentials alone as long as with them.
+//
+// Two kinds of work: a sequence's own rows over what it sees (splits of a
 // unit's tiles are joined by the last CTA to arrive, in order), or, for a
 // shared prefix, all sequences' rows over the prefix's tiles, whose partial
 // results (O, m, l) the streaming kernel joins with each sequence's own part.
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "kv_attend.cuh"
@@ -37,7 +46,7 @@ namespace paged {
 
 constexpr int KT = 128;                    // keys per tile
 constexpr int HALF = 128;                  // rows per half
-constexpr int TILE_THREADS = 16 * 32;    // warp 15 fills the last group
+constexpr int TILE_THREADS = 16 * 32;      // warp 15 fills the last group
 constexpr int UNITS = 3;                   // unit records in flight
 constexpr int PANEL = 128 * 128;           // bytes of 128 rows x 64 fp16
 constexpr int OFF_Q = 0;                   // [half][2 panels]
@@ -749,7 +758,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
                             f2{ff[x], ff[x]}, f2{mneg[x], mneg[x]});
                 a = f2{ex2(a.x), ex2(a.y)};
                 sum[x] = add2(sum[x], a);
-                f2 w = careful.value ? mul2(mul2(a, f2{svi, svi}), f2{sv.x, sv.y}) : mul2(a, f2{sv.x, sv.y});
+                // (scales first: the weights alone may pass float32's end with 1 / svr)
+                f2 w = mul2(a, careful.value ? mul2(f2{svi, svi}, f2{sv.x, sv.y}) : f2{sv.x, sv.y});
                 if (careful.value) {         // a hidden key's scale may be infinite or NaN
                   w.x = a.x == 0.f ? 0.f : w.x;
                   w.y = a.y == 0.f ? 0.f : w.y;
@@ -790,9 +800,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
       }
       tiles += n;
       if (!ok) break;
-      // ---- out
+      // ---- out.  Partial sums that large scales might carry past float32's end stand at 2^-40 of
+      // themselves, their reference 40 higher.
       const int pieces = u.pieces, slot = u.slot;
-      const bool split = pieces > 1 && !P.shared, live = row < rows;
+      const bool split = pieces > 1 && !P.shared, live = row < rows, down40 = (split || P.shared) && svr >= 1.0f;
+      if (down40) mr += 40.0f, lr *= 9.094947e-13f;
       const int at = u.base + min(row, rows - 1), tok = at / P.G, head = u.h * P.G + at - tok * P.G;
       const int64_t out_row = static_cast<int64_t>(u.row0 + tok) * P.hq + head;
       float* part_o = nullptr;               // partial results, and this row's place in them
@@ -817,7 +829,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
       if (active) {
         // through this half's queries, which nothing reads any more, so that 16 lanes store a row's
         // whole lines
-        const float inv = lr == 0.f ? 0.f : 1.0f / lr;
+        const float inv = part_o ? (down40 ? 9.094947e-13f : 1.0f) : lr == 0.f ? 0.f : 1.0f / lr;
         uint8_t* stage = smem + OFF_Q + hf * 2 * PANEL;
         const int lane_row = part_o ? static_cast<int>(part_row) : static_cast<int>(out_row);
         const int passes = part_o ? 2 : 1;
@@ -837,7 +849,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
 #pragma unroll
               for (int d = 0; d < 8; ++d) {
                 const float o = __uint_as_float(v[8 * c8 + place8<BITS>(d)]);
-                y[d] = n > 0 && lr != 0.f ? o * svr : 0.f;
+                y[d] = n > 0 && lr != 0.f ? o * inv * svr : 0.f;
               }
               if (part_o) {
                 const int at = 8 * (c & 1) + 2 * c8;
@@ -847,7 +859,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
                 uint32_t w[4];
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
-                  __nv_bfloat162 b2 = __floats2bfloat162_rn(y[2 * d] * inv, y[2 * d + 1] * inv);
+                  __nv_bfloat162 b2 = __floats2bfloat162_rn(y[2 * d], y[2 * d + 1]);
                   w[d] = *reinterpret_cast<uint32_t*>(&b2);
                 }
                 *reinterpret_cast<uint4*>(stage + chunk_at(r, 4 * c + c8)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -1097,9 +1109,15 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
 }
 
 sq_status launch_tile(const AttnParams& P, int bits, cudaStream_t stream) {
+  static std::atomic<bool> allowed[64][2];
   auto kern = bits == 8 ? tile_kernel<8> : tile_kernel<4>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TILE_SMEM);
-  if (e != cudaSuccess) return host::cuda_fail("cudaFuncSetAttribute(kv tile)", e);
+  const int d = host::current_device(), v = bits == 8;
+  cudaError_t e = cudaSuccess;
+  if (d < 0 || d >= 64 || !allowed[d][v].load()) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TILE_SMEM);
+    if (e != cudaSuccess) return host::cuda_fail("cudaFuncSetAttribute(kv tile)", e);
+    if (d >= 0 && d < 64) allowed[d][v].store(true);
+  }
   if (P.units < 1) return SQ_OK;
   const int64_t cap = host::num_sms();
   const int grid = static_cast<int>(P.units < cap ? P.units : cap);

@@ -308,6 +308,143 @@ def test_prefix_read_once(prefix, batch, new, hq, hkv, page, bits, rule):
     check(prob, *attend(prob))
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("new,own,hq,hkv,page", [
+    ([5, 8, 1, 0], [300, 200, 90, 5], 16, 4, 16),   # 20 and 32 rows: two units of 16
+    ([1] * 40, [(37 * i) % 900 for i in range(40)], 8, 8, 16),       # more units than CTAs: ragged pieces
+    ([1] * 60, [(13 * i) % 40 for i in range(60)], 32, 8, 32),       # units of one tile or none
+    ([1, 1], [2000, 1], 256, 64, 128),
+    ([1], [700], 256, 1, 64),                       # 256 rows for one token
+])
+def test_units(new, own, hq, hkv, page, bits):
+    prob = G.Attention(40, new, own, hq, hkv, page, bits, pad=1)
+    check(prob, *attend(prob))
+
+
+def problems_of_all_kinds():
+    """One of each path: split streaming, units in pieces, split tiles, tiles, both kernels, a prefix in line,
+    a prefix in a pass of its own."""
+    return [G.Attention(41, [1, 1], [5000, 70], 4, 1, 64, 4), G.Attention(42, [1] * 40, [200 + i for i in range(40)], 8, 8, 16, 8),
+            G.Attention(43, [40], [2500], 8, 2, 64, 4), G.Attention(44, [300, 200], [300, 500], 8, 2, 32, 8),
+            G.Attention(45, [1, 90], [800, 90], 8, 2, 16, 4), G.Attention(46, [1, 3], [20, 90], 8, 2, 16, 8, prefix=300),
+            G.Attention(47, [1] * 160, [1 + i % 30 for i in range(160)], 8, 4, 16, 4, prefix=1000)]
+
+
+def test_calls_of_all_kinds_share_a_workspace():
+    """One stream's calls use one workspace: what each leaves in it is what the next expects, in any order."""
+    probs = problems_of_all_kinds()
+    pages = [pages_of(p.pool) for p in probs]
+    first = [attend(p, g) for p, g in zip(probs, pages)]
+    rng = np.random.default_rng(48)
+    for i in rng.integers(0, len(probs), 60):
+        out, lse = attend(probs[i], pages[i])
+        n = sum(probs[i].new)
+        assert torch.equal(out[:n], first[i][0][:n]) and torch.equal(lse[:n], first[i][1][:n])
+    assert sq.device_status() == 0
+
+
+def test_two_streams_at_once():
+    probs = problems_of_all_kinds()
+    pages = [pages_of(p.pool) for p in probs]
+    first = [attend(p, g)[0] for p, g in zip(probs, pages)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for k in range(20):
+        with torch.cuda.stream(streams[k & 1]):
+            i = (3 * k + k // 2) % len(probs)
+            got.append((i, attend(probs[i], pages[i])[0]))
+    torch.cuda.synchronize()
+    for i, out in got:
+        n = sum(probs[i].new)
+        assert torch.equal(out[:n], first[i][:n])
+
+
+def test_captured_calls_of_all_kinds_side_by_side():
+    probs = problems_of_all_kinds()
+    held, eager = [], []
+    for p in probs:
+        pages, q = pages_of(p.pool), bf16(p.q)
+        args = (cu(p.table()), cu(p.cu), cu(np.array(p.own, np.int32)), max(p.new))
+        if p.prefix:
+            table = cu(p.prefix_table())
+            call = lambda out, a=args, g=pages, q=q, t=table, n=p.prefix: sq.kv_prefix_attention(q, g, t, n, *a, out=out)  # noqa: E731
+        else:
+            call = lambda out, a=args, g=pages, q=q: sq.kv_paged_attention(q, g, *a, out=out)  # noqa: E731
+        out = torch.zeros_like(q)
+        call(out)
+        eager.append(out.clone())
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            call(out)
+        held.append((graph, out, call))
+    streams = [torch.cuda.Stream() for _ in probs]
+    for _ in range(5):
+        for (graph, out, _), s in zip(held, streams):
+            with torch.cuda.stream(s):
+                out.zero_()
+                graph.replay()
+    torch.cuda.synchronize()
+    for (_, out, _), e in zip(held, eager):
+        assert torch.equal(out, e)
+
+
+def test_pages_of_several_sequences():
+    """Two sequences that begin with the same pages (a copied table): both read them."""
+    prob = G.Attention(49, [1, 1], [100, 100], 8, 2, 16, 4)
+    prob.pool.table[1, :5] = prob.pool.table[0, :5]
+    for key in "kv":
+        prob.values[key, 1] = np.concatenate([prob.values[key, 0][:80], prob.values[key, 1][80:]])
+    check(prob, *attend(prob))
+
+
+def test_pool_past_32_bit_offsets():
+    """The same rows in a small pool and behind 4 GB of pages give the same bits."""
+    hq, hkv, page, bits, n = 8, 8, 4096, 8, 1040                      # 1040 x 4 MB of codes each
+    rng = np.random.default_rng(50)
+    T = 300
+    x = bf16(G.round_bf16(rng.standard_normal((T, hq + 2 * hkv, D))))
+    outs = []
+    for total, use in ((3, [2, 0]), (n, [n - 1, n - 2])):
+        pages = sq.KVPages.empty(total, page, hkv, bits)
+        table = cu(np.array([use], np.int32))
+        cached = cu(np.array([page - 150], np.int32))
+        c = cu(np.array([0, T], np.int32))
+        q = sq.kv_paged_append(x[:, :hq], x[:, hq:2 * hq], x[:, 2 * hq:], pages, table, c, cached)
+        lengths = cu(np.array([page - 150 + T], np.int32))
+        args = dict(window=T)                                         # some rows in front, which hold zeros
+        many = sq.kv_paged_attention(q, pages, table, c, lengths, T, **args)
+        one = sq.kv_paged_attention(q[-1:], pages, table, cu(np.array([0, 1], np.int32)), lengths, 1, **args)
+        back = sq.kv_paged_dequant(pages, table, c, cached, T)
+        outs.append((many, one) + back)
+    assert sq.device_status() == 0
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    assert outs[1][0].abs().max() > 0
+
+
+@pytest.mark.parametrize("new,own", [([1], [300]), ([64], [300])])
+def test_rows_that_hold_zeros(new, own):
+    """Rows of a fresh pool (scale 0) stand for zeros: keys score 0 and values add nothing, whole tiles of them
+    in front of the first others too."""
+    prob = G.Attention(51, new, own, 4, 1, 16, 4)
+    for key in "kv":
+        for pos in range(200):
+            at = prob.pool.table[0, pos // 16], slice(None), pos % 16
+            for part in ("_codes", "_scale", "_zero"):
+                prob.pool.arrays[key + part][at] = 0
+        prob.values[key, 0][:200] = 0
+    check(prob, *attend(prob))
+
+
+@pytest.mark.parametrize("size", [1e-38, 1e-30, 1e-20, 1e20, 1e30, 1e36])
+@pytest.mark.parametrize("new", [1, 64])
+def test_value_scales_at_the_ends(new, size):
+    prob = G.Attention(52, [new], [300], 4, 1, 16, 4, v_size=size)
+    check(prob, *attend(prob))
+
+
 def test_many_rows_split_and_repeat():
     prob = G.Attention(36, [40, 3], [2500, 9], 8, 2, 64, 4)
     a = attend(prob)
