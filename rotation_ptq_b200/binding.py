@@ -158,10 +158,15 @@ def _need_cuda(*ts):
 SQ_ERR_TIMEOUT = 5
 
 
+_Tensor = torch.Tensor
+
+
 def _expect(t, name, dtype, shape):
     """Reject a tensor whose dtype, shape or layout the C entry point would
     misread (a short or mistyped buffer would be read or written past its end
     on the device)."""
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.dtype != dtype:
@@ -669,7 +674,7 @@ class KVPages:
 
 def _heads(t, name, heads=None):
     """A bf16 tensor [T, heads, 128] whose heads are contiguous; returns its token stride."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 3:
+    if not isinstance(t, _Tensor) or t.dtype is not torch.bfloat16 or t.dim() != 3:
         raise ValueError("%s must be a bf16 tensor [T, heads, 128]" % name)
     T, h, d = t.shape
     if d != 128 or (heads is not None and h != heads):
@@ -698,12 +703,14 @@ def _expect_batch(pages, block_table, cu_seqlens, lengths, lname):
     return B, width
 
 
-def _call_on(device_index, fn, *args):
-    """fn(*args) with the device current (the library launches on the current device)."""
-    if device_index == torch._C._cuda_getDevice():
-        return fn(*args)
-    with torch.cuda.device(device_index):
-        return fn(*args)
+def _enter(device_index):
+    """Makes the device current for a C call (the library launches on the current device); returns the
+    device to go back to, or None where nothing changed."""
+    current = torch._C._cuda_getDevice()
+    if device_index == current:
+        return None
+    torch.cuda.set_device(device_index)
+    return current
 
 
 def kv_paged_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pages: KVPages,
@@ -751,12 +758,18 @@ def kv_paged_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pages: KV
     _need_cuda(q, pages.k_codes)
     if q_out is None:
         q_out = torch.empty((T, hq, 128), dtype=torch.bfloat16, device=q.device)
-    st = _call_on(q.get_device(), lib.sq_kv_paged_append, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                  sq_, sk, sv, T, hq, pages._ref, block_table.data_ptr(), width,
-                  cu_seqlens.data_ptr(), cached.data_ptr(), B, _ptr(cos), _ptr(sin), max_pos, rot,
-                  int(bool(interleaved)), _ptr(q_norm), _ptr(k_norm), float(eps), q_out.data_ptr(),
-                  _stream(q))
-    _check(st, "sq_kv_paged_append")
+    back = _enter(q.get_device())
+    try:
+        st = lib.sq_kv_paged_append(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), sq_, sk, sv, T, hq, pages._ref,
+            block_table.data_ptr(), width, cu_seqlens.data_ptr(), cached.data_ptr(), B, _ptr(cos),
+            _ptr(sin), max_pos, rot, 1 if interleaved else 0, _ptr(q_norm), _ptr(k_norm), float(eps),
+            q_out.data_ptr(), _stream(q))
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
+    if st:
+        _check(st, "sq_kv_paged_append")
     return q_out
 
 
@@ -779,9 +792,14 @@ def kv_paged_dequant(pages: KVPages, block_table: torch.Tensor, cu_seqlens: torc
         k_out = torch.empty(shape, dtype=torch.bfloat16, device=pages.device)
     if v_out is None:
         v_out = torch.empty(shape, dtype=torch.bfloat16, device=pages.device)
-    st = _call_on(block_table.get_device(), lib.sq_kv_paged_dequant, pages._ref,
-                  block_table.data_ptr(), width, cu_seqlens.data_ptr(), cached.data_ptr(), B,
-                  shape[0], k_out.data_ptr(), v_out.data_ptr(), _stream(block_table))
+    back = _enter(block_table.get_device())
+    try:
+        st = lib.sq_kv_paged_dequant(pages._ref, block_table.data_ptr(), width,
+                                     cu_seqlens.data_ptr(), cached.data_ptr(), B, shape[0],
+                                     k_out.data_ptr(), v_out.data_ptr(), _stream(block_table))
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
     _check(st, "sq_kv_paged_dequant")
     return k_out, v_out
 
@@ -874,30 +892,35 @@ def _kv_attention(q, pages, prefix_table, prefix_len, block_table, cu_seqlens, l
     rule = _ScoreRule(128 ** -0.5 if scale is None else float(scale), float(softcap), int(window),
                       _ptr(slopes))
     max_q = int(max_q)
-    device = q.get_device()
     stream = _stream(q)
-    if workspace is None:
-        sizes = (T, hq, B, width, max_q, prefix_len)
-        need = pages._ws_bytes.get(sizes)
-        if need is None:
-            need = _call_on(device, kv_attention_workspace_bytes, T, hq, pages, B, width, max_q,
-                            prefix_len)
-            if len(pages._ws_bytes) >= 4096:
-                pages._ws_bytes.clear()
-            pages._ws_bytes[sizes] = need
-        workspace = _call_on(device, _attention_workspace, q.device, stream, need) if need else None
-    ws_ptr = None if workspace is None else workspace.data_ptr()
-    ws_bytes = 0 if workspace is None else workspace.numel()
-    args = (block_table.data_ptr(), width, cu_seqlens.data_ptr(), lengths.data_ptr(), B, max_q,
-            ctypes.addressof(rule), out.data_ptr(), _ptr(lse), ws_ptr, ws_bytes, stream)
-    if prefix_table is None:
-        st = _call_on(device, lib.sq_kv_paged_attention, q.data_ptr(), stride, T, hq, pages._ref,
-                      *args)
-        name = "sq_kv_paged_attention"
-    else:
-        st = _call_on(device, lib.sq_kv_prefix_attention, q.data_ptr(), stride, T, hq, pages._ref,
-                      prefix_table.data_ptr(), prefix_len, *args)
-        name = "sq_kv_prefix_attention"
+    back = _enter(q.get_device())
+    try:
+        if workspace is None:
+            sizes = (T, hq, B, width, max_q, prefix_len)
+            need = pages._ws_bytes.get(sizes)
+            if need is None:
+                need = kv_attention_workspace_bytes(T, hq, pages, B, width, max_q, prefix_len)
+                if len(pages._ws_bytes) >= 4096:
+                    pages._ws_bytes.clear()
+                pages._ws_bytes[sizes] = need
+            workspace = _attention_workspace(q.device, stream, need) if need else None
+        ws_ptr = None if workspace is None else workspace.data_ptr()
+        ws_bytes = 0 if workspace is None else workspace.numel()
+        if prefix_table is None:
+            name = "sq_kv_paged_attention"
+            st = lib.sq_kv_paged_attention(
+                q.data_ptr(), stride, T, hq, pages._ref, block_table.data_ptr(), width,
+                cu_seqlens.data_ptr(), lengths.data_ptr(), B, max_q, ctypes.addressof(rule),
+                out.data_ptr(), _ptr(lse), ws_ptr, ws_bytes, stream)
+        else:
+            name = "sq_kv_prefix_attention"
+            st = lib.sq_kv_prefix_attention(
+                q.data_ptr(), stride, T, hq, pages._ref, prefix_table.data_ptr(), prefix_len,
+                block_table.data_ptr(), width, cu_seqlens.data_ptr(), lengths.data_ptr(), B, max_q,
+                ctypes.addressof(rule), out.data_ptr(), _ptr(lse), ws_ptr, ws_bytes, stream)
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
     _check(st, name)
     return out
 

@@ -775,9 +775,9 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
           p[R * D + R + r] = ll[r];
         }
       }
-      __threadfence();
       __syncthreads();
       if (tid == 0) {
+        __threadfence();                   // the whole block's writes, which the barrier has ordered before
         const unsigned seen = atomicAdd(P.count + c0, 1u);
         sm_last = seen == static_cast<unsigned>(c1 - c0);
         if (sm_last) P.count[c0] = 0;
