@@ -201,6 +201,10 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
   __shared__ bool sm_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int G = P.G, hkv = P.pages.hkv, B = P.batch.B;
+  // a programmatic dependent.  Behind a shared prefix's pass its CTAs begin with the sequences' own keys
+  // as that pass's end (it has waited for what was before it), and wait where they join
+  if (P.ex_n == 0) griddep_wait();
+  griddep_launch_dependents();
   const bool split = P.part != nullptr;
 
   // ---- the list: this CTA's piece, and the sequence it begins in
@@ -715,8 +719,36 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
     // largest reference first, then 128 / R pieces' factors at a time by one thread each, so that
     // every load but the factors' is independent
     auto join = [&](int n, auto ml, auto out) {
-      constexpr int STEP = THREADS / R, AHEAD = 64 / R;
+      constexpr int STEP = THREADS / R, AHEAD = 32 / R;
       const int jr = tid % R, jq = tid / R;
+      if (n <= AHEAD) {                    // few pieces: everything at once
+        float2 q[AHEAD][R];
+        float po[AHEAD][R];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            q[k][r] = ml(min(k, n - 1), r);
+            po[k][r] = out(min(k, n - 1), r);
+          }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float x = mm[r];
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) x = fmaxf(x, q[k][r].x);
+          float f = mm[r] == -INFINITY ? 0.f : ex2(mm[r] - x);
+          acc[r] = f != 0.f ? acc[r] * f : 0.f;
+          ll[r] *= f;
+          mm[r] = x;
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) {
+            f = k >= n || q[k][r].x == -INFINITY ? 0.f : ex2(q[k][r].x - x);
+            if (f != 0.f) acc[r] = fmaf(f, po[k][r], acc[r]);
+            ll[r] = fmaf(f, q[k][r].y, ll[r]);
+          }
+        }
+        return;
+      }
       const float2 mine = jq < n ? ml(jq, jr) : make_float2(-INFINITY, 0.f);
       float top = mine.x;
       for (int q = jq + STEP; q < n; q += STEP) top = fmaxf(top, ml(q, jr).x);
@@ -992,19 +1024,7 @@ sq_status run_attention(const void* q, int64_t q_stride, int64_t T, int hq,
   P.ex_n = plan.shared ? plan.tile_split : 0;
   const int grid = stream_grid(pages.bits, plan.kind);
   const StreamKernel k = stream_of(pages.bits, plan.kind);
-  // behind a pass over the shared prefix: a programmatic dependent, whose CTAs begin with the sequences'
-  // own keys as that pass's end
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(THREADS, 1, 1);
-  cfg.dynamicSmemBytes = k.smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = plan.shared ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k.fn, P);
+  const cudaError_t e = host::launch_dependent(k.fn, grid, THREADS, k.smem, stream, P);
   return e == cudaSuccess ? SQ_OK : host::cuda_fail("kv attention launch", e);
 }
 

@@ -251,6 +251,8 @@ __device__ __forceinline__ void store_quantized(const float (&y)[16], int s, uns
 // WHOLE: half layout over the whole head.
 template <int BITS, bool WHOLE>
 __global__ void __launch_bounds__(256, 3) append_kernel(const AppendParams P) {
+  griddep_wait();
+  griddep_launch_dependents();
   const int lane = threadIdx.x & 31, s = lane & (LPV - 1), vec = lane / LPV;
   const unsigned mask = 0xFFu << (lane & 24);
   const int jobs = P.jq + 2 * P.jk;        // four heads each: Q, K, V
@@ -342,6 +344,8 @@ template <int BITS>
 __global__ void __launch_bounds__(256) dequant_kernel(const Pages P, const Batch b, __nv_bfloat16* k_out,
                                                       __nv_bfloat16* v_out, int split) {
   constexpr int RB = D * BITS / 8;
+  griddep_wait();
+  griddep_launch_dependents();
   const int lane = threadIdx.x & 31, c = lane & 15;
   const bool is_v = lane >= 16;            // a job: one head's K and V
   const uint8_t* codes = is_v ? P.vc : P.kc;
@@ -423,8 +427,8 @@ sq_status run_append(const void* q, const void* k, const void* v, int64_t q_stri
   const bool whole = cos && rot == D && !interleaved;
   auto kern = pages.bits == 8 ? (whole ? append_kernel<8, true> : append_kernel<8, false>)
                               : (whole ? append_kernel<4, true> : append_kernel<4, false>);
-  kern<<<grid_for(T * P.split, 8), 256, 0, stream>>>(P);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      host::launch_dependent(kern, grid_for(T * P.split, 8), 256, 0, stream, P);
   return e == cudaSuccess ? SQ_OK : host::cuda_fail("kv_paged_append launch", e);
 }
 
@@ -433,10 +437,10 @@ sq_status run_dequant(const sq_kv_pages& pages, const int32_t* table, int width,
                       cudaStream_t stream) {
   auto kern = pages.bits == 8 ? dequant_kernel<8> : dequant_kernel<4>;
   const int split = warps_per_token(T, pages.hkv);
-  kern<<<grid_for(T * split, 8), 256, 0, stream>>>(
-      view(pages), Batch{table, cu, cached, width, B, T}, static_cast<__nv_bfloat16*>(k_out),
+  const cudaError_t e = host::launch_dependent(
+      kern, grid_for(T * split, 8), 256, 0, stream, view(pages),
+      Batch{table, cu, cached, width, B, T}, static_cast<__nv_bfloat16*>(k_out),
       static_cast<__nv_bfloat16*>(v_out), split);
-  cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SQ_OK : host::cuda_fail("kv_paged_dequant launch", e);
 }
 

@@ -252,9 +252,41 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
-// (a, b) *= (x, y), floats held in registers of tensor-memory transfers.
-__device__ __forceinline__ void mul2u(uint32_t& a, uint32_t& b, float x, float y) {
-  const f2 r = mul2(f2{__uint_as_float(a), __uint_as_float(b)}, f2{x, y});
+// Pairs of floats as the 64-bit registers that f32x2 instructions take: a pair that stays (a row's
+// factor, twice) is put together once.
+using pair_t = unsigned long long;
+__device__ __forceinline__ pair_t pair_of(uint32_t x, uint32_t y) {
+  pair_t p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(x), "r"(y));
+  return p;
+}
+__device__ __forceinline__ pair_t pair_of(float x, float y) {
+  return pair_of(__float_as_uint(x), __float_as_uint(y));
+}
+__device__ __forceinline__ float2 floats_of(pair_t p) {
+  uint32_t x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(p));
+  return make_float2(__uint_as_float(x), __uint_as_float(y));
+}
+__device__ __forceinline__ pair_t pair_mul(pair_t a, pair_t b) {
+  pair_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ pair_t pair_add(pair_t a, pair_t b) {
+  pair_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ pair_t pair_fma(pair_t a, pair_t b, pair_t c) {
+  pair_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// (a, b) *= p, floats held in registers of tensor-memory transfers.
+__device__ __forceinline__ void mul2u(uint32_t& a, uint32_t& b, pair_t p) {
+  const float2 r = floats_of(pair_mul(pair_of(a, b), p));
   a = __float_as_uint(r.x);
   b = __float_as_uint(r.y);
 }
@@ -462,7 +494,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t spin = P.spin_limit;
 
-  if (P.shared) griddep_launch_dependents();           // the streaming kernel that joins
+  // a programmatic dependent; what follows may be set up from here on (behind a shared prefix's pass it
+  // is the streaming kernel that joins, which relies on this wait for the call's inputs)
+  griddep_wait();
+  griddep_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.k_full[i], 4);
@@ -497,10 +532,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
   TileUnit* ring_u = reinterpret_cast<TileUnit*>(smem + OFF_UNITS);
   bool ok = true;
 
-  // registers, of the 512 x 128 that the block is launched with: 128 x (2 x 152 + 104 + 104)
+  // registers, of the 512 x 128 that the block is launched with: 128 x (2 x 192 + 64 + 64) at 4 bits,
+  // 128 x (2 x 184 + 88 + 56) at 8
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(BITS == 4 ? 176 : 168));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(BITS == 4 ? 192 : 184));
     const int hf = warp >> 2, quarter = warp & 3;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const uint32_t t_s0 = lane_base + hf * 128, t_o = lane_base + 256 + hf * 128;
@@ -582,19 +618,23 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.q_full[hf]);
-        float f[4], slope[4], mneg[4];
+        float f[4], slope[4];
         int qpos[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           f[x] = __shfl_sync(0xffffffffu, row_f, 8 * x + g);
           slope[x] = -__shfl_sync(0xffffffffu, row_slope, 8 * x + g);
           qpos[x] = __shfl_sync(0xffffffffu, row_pos, 8 * x + g);
-          mneg[x] = 0.f;
         }
         const int qmin = __reduce_min_sync(0xffffffffu, row_pos), qmax = __reduce_max_sync(0xffffffffu, row_pos);
         float ff[4];                         // the scores' factor inside the exponential
+        pair_t ff2[4], mneg2[4];             // twice each: it, and the reference taken off
 #pragma unroll
-        for (int x = 0; x < 4; ++x) ff[x] = special ? 1.0f : f[x];
+        for (int x = 0; x < 4; ++x) {
+          ff[x] = special ? 1.0f : f[x];
+          ff2[x] = pair_of(ff[x], ff[x]);
+          mneg2[x] = pair_of(0.f, 0.f);
+        }
 
         for (int j = 0; j < steps; ++j) {
           const int tile = tiles + (j >> 1), ring = tile & 3, b = j & 1, key0 = b * (KT / 2);
@@ -608,15 +648,15 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           tc_fence_after();
           const uint32_t t_s = t_s0 + key0;
           // this lane's pairs of scales: keys 8 c + 2 t, + 1
-          const float2* sk2 = reinterpret_cast<const float2*>(s_sk + ring * KT + key0) + t;
-          const float2* sv2 = reinterpret_cast<const float2*>(s_sv + ring * KT + key0) + t;
+          const pair_t* sk2 = reinterpret_cast<const pair_t*>(s_sk + ring * KT + key0) + t;
+          const pair_t* sv2 = reinterpret_cast<const pair_t*>(s_sv + ring * KT + key0) + t;
           const int kpos = tile_pos(P, u, j >> 1) + key0;
           if (P.cap > 0.f) {
             // capped scores, in log2 units, back to tensor memory
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
               uint32_t w[2][4];
-              const float2 sk = sk2[4 * c];
+              const float2 sk = floats_of(sk2[4 * c]);
 #pragma unroll
               for (int bk = 0; bk < 2; ++bk) tmem_ld_16x256b_x1(t_s + (bk << 20) + 8 * c, w[bk]);
               tmem_ld_wait();
@@ -643,10 +683,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           if (P.cap <= 0.f) {
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              const float2 sk = sk2[4 * c];
+              const pair_t sk = sk2[4 * c];
 #pragma unroll
               for (int x = 0; x < 4; ++x)
-                mul2u(v[x >> 1][4 * c + 2 * (x & 1)], v[x >> 1][4 * c + 2 * (x & 1) + 1], sk.x, sk.y);
+                mul2u(v[x >> 1][4 * c + 2 * (x & 1)], v[x >> 1][4 * c + 2 * (x & 1) + 1], sk);
             }
           }
           if (P.slopes != nullptr) {
@@ -716,8 +756,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
               m[x] = nm;
               l[x] *= fa;
               g4[x] = fa * down;
-              mneg[x] = nm == -INFINITY ? 0.f : -nm;
-              if (!far) mneg[x] -= static_cast<float>(static_cast<int>(__float_as_uint(svr) >> 23) - 127);
+              float off = nm == -INFINITY ? 0.f : -nm;
+              if (!far) off -= static_cast<float>(static_cast<int>(__float_as_uint(svr) >> 23) - 127);
+              mneg2[x] = pair_of(off, off);
             }
             if (j > 0) {
               // the product of the step before; its barrier's phase before that was done when these
@@ -743,26 +784,25 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
             }
           }
           // ---- weights
-          f2 sum[4] = {f2{0.f, 0.f}, f2{0.f, 0.f}, f2{0.f, 0.f}, f2{0.f, 0.f}};
+          pair_t sum[4] = {0, 0, 0, 0};
           uint32_t o[2][16];
           // (the common case is compiled by itself: branches inside cost it half its rate)
           auto weights = [&](auto careful) {
             const float svi = !far ? 1.0f : svr > 0.f ? 1.0f / svr : 0.f;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              const float2 sv = sv2[4 * c];
+              const pair_t sv = careful.value ? pair_mul(sv2[4 * c], pair_of(svi, svi)) : sv2[4 * c];
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 const int at = 4 * c + 2 * (x & 1);
-                f2 a = fma2(f2{__uint_as_float(v[x >> 1][at]), __uint_as_float(v[x >> 1][at + 1])},
-                            f2{ff[x], ff[x]}, f2{mneg[x], mneg[x]});
-                a = f2{ex2(a.x), ex2(a.y)};
-                sum[x] = add2(sum[x], a);
-                // (scales first: the weights alone may pass float32's end with 1 / svr)
-                f2 w = mul2(a, careful.value ? mul2(f2{svi, svi}, f2{sv.x, sv.y}) : f2{sv.x, sv.y});
+                const float2 y = floats_of(pair_fma(pair_of(v[x >> 1][at], v[x >> 1][at + 1]), ff2[x], mneg2[x]));
+                const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                const pair_t a = pair_of(e.x, e.y);
+                sum[x] = pair_add(sum[x], a);
+                float2 w = floats_of(pair_mul(a, sv));
                 if (careful.value) {         // a hidden key's scale may be infinite or NaN
-                  w.x = a.x == 0.f ? 0.f : w.x;
-                  w.y = a.y == 0.f ? 0.f : w.y;
+                  w.x = e.x == 0.f ? 0.f : w.x;
+                  w.y = e.y == 0.f ? 0.f : w.y;
                 }
                 o[x >> 1][2 * c + (x & 1)] = h2_bits(__floats2half2_rn(w.x, w.y));
               }
@@ -775,7 +815,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
 #pragma unroll
           for (int bk = 0; bk < 2; ++bk) tmem_st_16x128b_x8(t_s + (bk << 20), o[bk]);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) l[x] += (sum[x].x + sum[x].y) * (far ? 1.0f : svr);
+          for (int x = 0; x < 4; ++x) {
+            const float2 s2 = floats_of(sum[x]);
+            l[x] += (s2.x + s2.y) * (far ? 1.0f : svr);
+          }
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -962,7 +1005,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
     }
   } else if (warp < 12) {
     // ----------------------------------------------------------- widening
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(BITS == 4 ? 80 : 104));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(BITS == 4 ? 64 : 88));
     const int pw = warp - 8, t = lane & 3, b3 = lane >> 2;
     // rows of a warp's load instruction; the two rows of a store phase differ in a bit that the
     // lanes' chunks do not use (see widen_rows)
@@ -1069,7 +1112,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
     }
   } else {
     // ------------------------------------------------------------ products
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(BITS == 4 ? 80 : 72));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(BITS == 4 ? 64 : 56));
     // one warp per half, which sleeps while its half has nothing to do: a single one that polls both
     // halves' barriers takes issue slots and shared memory from the warps that work
     if (warp == 12) {
@@ -1121,8 +1164,7 @@ sq_status launch_tile(const AttnParams& P, int bits, cudaStream_t stream) {
   if (P.units < 1) return SQ_OK;
   const int64_t cap = host::num_sms();
   const int grid = static_cast<int>(P.units < cap ? P.units : cap);
-  kern<<<grid, TILE_THREADS, TILE_SMEM, stream>>>(P);
-  e = cudaGetLastError();
+  e = host::launch_dependent(kern, grid, TILE_THREADS, TILE_SMEM, stream, P);
   return e == cudaSuccess ? SQ_OK : host::cuda_fail("kv tile launch", e);
 }
 

@@ -27,6 +27,24 @@ uint32_t spin_limit();
 // GEMM kernel selection set by sq_debug_set_gemm_path (0 = automatic).
 int gemm_path();
 
+// Launches a kernel as a programmatic dependent: it may be set up while the
+// one before it in the stream drains, and begins with griddepcontrol.wait.
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*fn)(Params...), int grid, int threads, size_t smem,
+                             cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
 }  // namespace host
 
 namespace gemm {
