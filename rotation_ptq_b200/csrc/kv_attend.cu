@@ -218,77 +218,107 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
   // a unit's beginning and end count as kOverhead tiles (a batch of ragged lengths would else leave
   // the CTAs with the short ones behind: 101 against 62 us).
   int64_t tiles = 0, units = 0;
-  for (int b = bfirst; b < blast; ++b) {
-    const Seq s = load_seq(P, b, blockIdx.x == 0);
-    units += count(s);
-    tiles += count(s) * max(s.tiles(), 1);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    units += __shfl_xor_sync(0xffffffffu, units, o);
-    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
-  }
-  if (lane == 0) {
-    sm_scan[warp] = units;
-    sm_scan[WARPS + warp] = tiles;
-  }
-  __syncthreads();
-  units = tiles = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    units += sm_scan[w];
-    tiles += sm_scan[WARPS + w];
-  }
-  const bool slots = split && 2 * units <= gridDim.x;
-  const int per_slot = slots ? static_cast<int>(min(tiles / (gridDim.x - units) + 1, static_cast<int64_t>(1 << 30))) : 1;
+  bool slots = false;
+  int per_slot = 1;
   // places of a unit in the list: slots, or tiles behind kOverhead; a unit without keys still writes zeros
   auto places = [&](const Seq& s) {
     const int n = max(s.tiles(), 1);
     return !split ? 1 : slots ? (n + per_slot - 1) / per_slot : n + kOverhead;
   };
-  int64_t mine = 0;
-  for (int b = bfirst; b < blast; ++b) {
-    const Seq s = load_seq(P, b, false);
-    mine += count(s) * places(s);
-  }
-  int64_t incl = mine;
+  auto choose = [&]() {
+    slots = split && 2 * units <= gridDim.x;
+    if (slots) per_slot = static_cast<int>(min(tiles / (gridDim.x - units) + 1, static_cast<int64_t>(1 << 30)));
+  };
+  auto warp_sum = [&](int64_t v) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  __syncthreads();
-  if (lane == 31) sm_scan[warp] = incl;
-  __syncthreads();
-  int64_t before = 0, total = 0;
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  auto warp_scan = [&](int64_t v) {        // inclusive
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    if (w < warp) before += sm_scan[w];
-    total += sm_scan[w];
-  }
-  const int64_t excl = before + incl - mine;
-  // equal pieces but for the last; a unit's pieces belong to consecutive CTAs
-  const int64_t piece = slots ? 1 : (total + gridDim.x - 1) / gridDim.x;
-  const int64_t r0 = piece * blockIdx.x, r1 = min(total, r0 + piece);
-  if (r0 >= r1) {
-    griddep_wait();                        // this kernel's end tells that of the shared prefix's pass too
-    return;
-  }
-  if (r0 >= excl && r0 < excl + mine) {
-    int b = bfirst;
-    int64_t base = excl;
-    for (;; ++b) {
-      const Seq s = load_seq(P, b, false);
-      const int64_t w = count(s) * places(s);
-      if (r0 < base + w) break;
-      base += w;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
     }
-    sm_b = b;
-    sm_base = base;
+    return v;
+  };
+  int64_t total, base, piece, r0, r1;
+  int b;
+  // equal pieces but for the last; a unit's pieces belong to consecutive CTAs
+  auto cut = [&]() {
+    piece = slots ? 1 : (total + gridDim.x - 1) / gridDim.x;
+    r0 = piece * blockIdx.x;
+    r1 = min(total, r0 + piece);
+    if (r0 < r1) return true;
+    griddep_wait();                        // this kernel's end tells that of the shared prefix's pass too
+    return false;
+  };
+  if (B <= 32) {
+    // every warp by itself, a lane per sequence: no barriers
+    const Seq s = load_seq(P, min(lane, B - 1), blockIdx.x == 0 && tid < B);
+    const int64_t n = lane < B ? count(s) : 0;
+    units = warp_sum(n);
+    tiles = warp_sum(n * max(s.tiles(), 1));
+    choose();
+    const int64_t w = n * places(s), incl = warp_scan(w);
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    if (!cut()) return;
+    b = __ffs(__ballot_sync(0xffffffffu, r0 < incl)) - 1;
+    base = __shfl_sync(0xffffffffu, incl - w, b);
+  } else {
+    for (int q = bfirst; q < blast; ++q) {
+      const Seq s = load_seq(P, q, blockIdx.x == 0);
+      units += count(s);
+      tiles += count(s) * max(s.tiles(), 1);
+    }
+    units = warp_sum(units);
+    tiles = warp_sum(tiles);
+    if (lane == 0) {
+      sm_scan[warp] = units;
+      sm_scan[WARPS + warp] = tiles;
+    }
+    __syncthreads();
+    units = tiles = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      units += sm_scan[w];
+      tiles += sm_scan[WARPS + w];
+    }
+    choose();
+    int64_t mine = 0;
+    for (int q = bfirst; q < blast; ++q) {
+      const Seq s = load_seq(P, q, false);
+      mine += count(s) * places(s);
+    }
+    const int64_t incl = warp_scan(mine);
+    __syncthreads();
+    if (lane == 31) sm_scan[warp] = incl;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) before += sm_scan[w];
+      total += sm_scan[w];
+    }
+    const int64_t excl = before + incl - mine;
+    if (!cut()) return;
+    if (r0 >= excl && r0 < excl + mine) {
+      int q = bfirst;
+      int64_t at = excl;
+      for (;; ++q) {
+        const Seq s = load_seq(P, q, false);
+        const int64_t w = count(s) * places(s);
+        if (r0 < at + w) break;
+        at += w;
+      }
+      sm_b = q;
+      sm_base = at;
+    }
+    __syncthreads();
+    b = sm_b;
+    base = sm_base;
   }
-  __syncthreads();
-  int b = sm_b;
-  int64_t base = sm_base;
 
   for (int64_t cur = r0; cur < r1;) {
     Unit u;
