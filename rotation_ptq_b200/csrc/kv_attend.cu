@@ -951,6 +951,7 @@ constexpr int kFewRows = 32;
 // behind 2000 65 / 55; 5 new tokens each, 6 sequences behind 2000 39 / 47, 32 behind 2000 108 / 89.
 constexpr int kSharedRows = 128;
 constexpr int kSharedTiles = 30;
+constexpr size_t kSharedBytes = size_t{1} << 30;          // of partial results: larger batches stream
 constexpr int kTileRows = 256;
 constexpr size_t kPartFloats = static_cast<size_t>(kTileRows) * (D + 2);
 
@@ -963,7 +964,8 @@ AttnPlan make_plan(int64_t T, int hq, int hkv, int B, int max_q, int64_t keys, i
   const int64_t per_unit = stream_of(bits, p.kind).rows;
   p.shared = have_ws && B > 1 && prefix_len > 0 && rows <= kSharedRows &&
              B * ((rows + per_unit - 1) / per_unit) * hkv * ((prefix_len + TILE - 1) / TILE) >=
-                 static_cast<int64_t>(kSharedTiles) * sms;
+                 static_cast<int64_t>(kSharedTiles) * sms &&
+             static_cast<size_t>(T) * hq * D * 4 <= kSharedBytes;
   p.tile = !p.shared && rows > kFewRows;
   p.stream = p.shared || !p.tile || B > 1;
   p.tile_split = 1;

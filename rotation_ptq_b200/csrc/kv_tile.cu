@@ -494,10 +494,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t spin = P.spin_limit;
 
-  // a programmatic dependent; what follows may be set up from here on (behind a shared prefix's pass it
-  // is the streaming kernel that joins, which relies on this wait for the call's inputs)
-  griddep_wait();
-  griddep_launch_dependents();
+  griddep_wait();                          // a programmatic dependent
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.k_full[i], 4);
@@ -529,6 +526,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
+  // What follows may be set up from here on: not before this kernel has its tensor memory, which a
+  // follower that waits for this kernel's end might else hold.  Behind a shared prefix's pass it is the
+  // streaming kernel that joins; it relies on the wait above for the call's inputs.
+  griddep_launch_dependents();
   TileUnit* ring_u = reinterpret_cast<TileUnit*>(smem + OFF_UNITS);
   bool ok = true;
 

@@ -1,5 +1,9 @@
 """The paged KV cache on the GPU against the float64 oracle: append, read-back, attention over pages and
 behind a shared prefix, and the calls one after another as a server makes them."""
+import pathlib
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -388,6 +392,71 @@ def test_captured_calls_of_all_kinds_side_by_side():
     torch.cuda.synchronize()
     for (_, out, _), e in zip(held, eager):
         assert torch.equal(out, e)
+
+
+def test_a_first_call_may_be_captured():
+    """In a process that has made no call yet: nothing that the first call sets up is in the way of capture."""
+    code = """
+import torch, rotation_ptq_b200 as sq
+pages = sq.KVPages.empty(64, 16, 2, 4)
+table = torch.arange(64, dtype=torch.int32, device="cuda").view(2, 32)
+q = torch.randn(41, 8, 128, device="cuda").bfloat16()
+kv = q[:, :2].contiguous()
+cu = torch.tensor([0, 1, 41], dtype=torch.int32, device="cuda")
+cached, lengths = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([300, 60], [301, 100]))
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    r = sq.kv_paged_append(q, kv, kv, pages, table, cu, cached)
+    out = sq.kv_paged_attention(r, pages, table, cu, lengths, 40)
+g.replay()
+torch.cuda.synchronize()
+want = sq.kv_paged_attention(r, pages, table, cu, lengths, 40)
+assert torch.equal(out, want) and out.isfinite().all() and sq.device_status() == 0
+"""
+    root = pathlib.Path(__file__).resolve().parents[1]
+    run = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
+
+
+def test_among_the_linear_layers():
+    """Attention calls and linear layers one behind the other without a gap, as in a model's step: kernels that
+    hold tensor memory and programmatic dependents in both orders."""
+    probs = problems_of_all_kinds()
+    pages = [pages_of(p.pool) for p in probs]
+    first = [attend(p, g)[0] for p, g in zip(probs, pages)]
+    rng = np.random.default_rng(53)
+    N, K = 512, 1024
+    w_q, w_s = cu(rng.integers(0, 256, (N, K // 2)).astype(np.uint8)), cu(rng.random(N).astype(np.float32))
+    layers = []
+    for M in (1, 16, 300):
+        a_q, a_s = cu(rng.integers(0, 256, (M, K // 2)).astype(np.uint8)), cu(rng.random(M).astype(np.float32))
+        layers.append((a_q, a_s, sq.w4a4_linear(a_q, a_s, w_q, w_s)))
+    torch.cuda.synchronize()
+    calls = []
+    for p, g in zip(probs, pages):
+        q = bf16(p.q)
+        args = (cu(p.table()), cu(p.cu), cu(np.array(p.own, np.int32)), max(p.new))
+        table = cu(p.prefix_table()) if p.prefix else None
+        calls.append((p, g, q, args, table))
+    torch.cuda.synchronize()
+    got, lin = [], []
+    for k in range(60):
+        i = int(rng.integers(0, len(calls)))
+        p, g, q, args, table = calls[i]
+        if p.prefix:
+            got.append((i, sq.kv_prefix_attention(q, g, table, p.prefix, *args)))
+        else:
+            got.append((i, sq.kv_paged_attention(q, g, *args)))
+        j = int(rng.integers(0, len(layers)))
+        lin.append((j, sq.w4a4_linear(layers[j][0], layers[j][1], w_q, w_s)))
+    torch.cuda.synchronize()
+    for i, out in got:
+        n = sum(probs[i].new)
+        assert torch.equal(out[:n], first[i][:n])
+    for j, out in lin:
+        assert torch.equal(out, layers[j][2])
+    assert sq.device_status() == 0
 
 
 def test_pages_of_several_sequences():
