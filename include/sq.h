@@ -632,7 +632,9 @@ typedef struct {
  *     out = sum_j softmax_j(s) v_hat_j,   lse = ln sum_j exp(s),
  * over the visible j <= p.  Products with the codes are exact and sums are in
  * float32; the output is rounded once to bf16.  A row with no visible key (p < 0) gets
- * zeros and lse -inf.
+ * zeros and lse -inf.  Weights of the softmax are held to 22 bits for sequences
+ * of up to 32 rows (new tokens x hq / hkv), to 11 bits (fp16) for more and over a
+ * prefix that is read once for the batch.
  *
  * q          device bf16 [T][hq][d] (q_out of the append), heads contiguous,
  *            q_stride elements between tokens (a multiple of 8).
@@ -647,8 +649,9 @@ typedef struct {
  * workspace  device scratch of sq_kv_attention_workspace_bytes() bytes, zero
  *            on first use and left zero where it must be by every call that
  *            finishes; one call at a time per workspace.  With less (or NULL)
- *            the keys of a row are not split across CTAs: the same result but
- *            for the order of float32 sums, and slower.
+ *            the keys of a row are not split across CTAs and a shared prefix
+ *            is read for every sequence: the same result but for the order of
+ *            float32 sums, and slower.
  * Shape rules: as sq_kv_paged_append; table_width * page_size < 2^30,
  * T * hq < 2^31.  (The workspace's size goes with all sizes of the call;
  * prefix_len is 0 for sq_kv_paged_attention.) */
@@ -666,7 +669,7 @@ sq_status sq_kv_paged_attention(const void* q, int64_t q_stride, int64_t T, int 
  * prefix_table (device int32 [ceil(prefix_len / page_size)]), the same for
  * all, and sequence b's own cache row j (lengths[b] of them, in its
  * block_table) is position prefix_len + j.  The shared rows are read once for
- * the batch.  prefix_len (host) is 1 .. 2^30 - 1; lengths[b] may be 0.  All
+ * the batch where that is less work than for each sequence.  prefix_len (host) is 1 .. 2^30 - 1; lengths[b] may be 0.  All
  * else as sq_kv_paged_attention; keys appended behind a prefix need their
  * rotary positions shifted by prefix_len (a table that starts there). */
 sq_status sq_kv_prefix_attention(const void* q, int64_t q_stride, int64_t T, int hq,

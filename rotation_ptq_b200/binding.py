@@ -841,7 +841,7 @@ def kv_prefix_attention(q: torch.Tensor, pages: KVPages, prefix_table: torch.Ten
     """kv_paged_attention behind a shared prefix (``sq_kv_prefix_attention``):
     the first prefix_len positions of every sequence are the rows of the pages
     prefix_table (int32 [pages]); lengths counts each sequence's own rows
-    behind them.  The prefix is read once for the batch.
+    behind them.  The prefix is read once for the batch where that pays.
     """
     if not isinstance(prefix_table, torch.Tensor) or prefix_table.dim() != 1:
         raise ValueError("prefix_table must be int32 [pages]")
