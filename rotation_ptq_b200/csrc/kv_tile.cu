@@ -481,7 +481,8 @@ __device__ __forceinline__ void issue_products(const AttnParams& P, uint8_t* sme
   __syncwarp();
 }
 
-template <int BITS>
+// SPECIAL: scores with a cap or slopes.  Without them the softmax is a third less code.
+template <int BITS, bool SPECIAL>
 __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams P) {
   constexpr int RB = D * BITS / 8;
   extern __shared__ uint8_t tile_smem_raw[];
@@ -545,7 +546,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
     const int g = lane >> 2, t = lane & 3;
     int tiles = 0, splits = 0;             // tiles seen by the CTA; joins
     uint32_t par_s = 0, par_o = 0;         // bit b: parities that come next, s_full[b] and o_full[b]
-    const bool special = P.cap > 0.f || P.slopes != nullptr;
     for (int k = 0; ok; ++k) {
       ok = __all_sync(0xffffffffu, mbar_wait(&bar.u_full[k % UNITS], (k / UNITS) & 1, spin));
       if (!ok) break;
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
         pair_t ff2[4], mneg2[4];             // twice each: it, and the reference taken off
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          ff[x] = special ? 1.0f : f[x];
+          ff[x] = SPECIAL ? 1.0f : f[x];
           ff2[x] = pair_of(ff[x], ff[x]);
           mneg2[x] = pair_of(0.f, 0.f);
         }
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           const pair_t* sk2 = reinterpret_cast<const pair_t*>(s_sk + ring * KT + key0) + t;
           const pair_t* sv2 = reinterpret_cast<const pair_t*>(s_sv + ring * KT + key0) + t;
           const int kpos = tile_pos(P, u, j >> 1) + key0;
-          if (P.cap > 0.f) {
+          if (SPECIAL && P.cap > 0.f) {
             // capped scores, in log2 units, back to tensor memory
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           const uint32_t flags = fl.x | fl.y | fl.z | fl.w;
           const bool edge = flags != 0u || kpos + KT / 2 - 1 > qmin || (P.window > 0 && qmax - kpos >= P.window);
           tmem_ld_wait();
-          if (P.cap <= 0.f) {
+          if (!SPECIAL || P.cap <= 0.f) {
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               const pair_t sk = sk2[4 * c];
@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
                 mul2u(v[x >> 1][4 * c + 2 * (x & 1)], v[x >> 1][4 * c + 2 * (x & 1) + 1], sk);
             }
           }
-          if (P.slopes != nullptr) {
+          if (SPECIAL && P.slopes != nullptr) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const float d0 = static_cast<float>(qpos[x] - kpos - 2 * t), fx = P.cap > 0.f ? 1.0f : f[x];
@@ -1153,9 +1153,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
 }
 
 sq_status launch_tile(const AttnParams& P, int bits, cudaStream_t stream) {
-  static std::atomic<bool> allowed[64][2];
-  auto kern = bits == 8 ? tile_kernel<8> : tile_kernel<4>;
-  const int d = host::current_device(), v = bits == 8;
+  static std::atomic<bool> allowed[64][4];
+  const bool special = P.cap > 0.f || P.slopes != nullptr;
+  auto kern = bits == 8 ? (special ? tile_kernel<8, true> : tile_kernel<8, false>)
+                        : (special ? tile_kernel<4, true> : tile_kernel<4, false>);
+  const int d = host::current_device(), v = (bits == 8 ? 2 : 0) + special;
   cudaError_t e = cudaSuccess;
   if (d < 0 || d >= 64 || !allowed[d][v].load()) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TILE_SMEM);
