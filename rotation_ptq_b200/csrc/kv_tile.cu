@@ -23,9 +23,12 @@
 // a slack, so that few steps rescale; the softmax in the fragment layout, where
 // a lane needs the scales of a quarter of the keys (with a thread per row every
 // lane reads them all: those broadcasts and the products' operand reads, both
-// from shared memory, slow one another 1.5 times).  What bounds it now is the
-// softmax's own latency: without its arithmetic the rest takes 275 us, without
-// the products' 460, without the exponentials alone as long as with them.
+// from shared memory, slow one another 1.5 times); caps and slopes compiled by
+// themselves, 546 to 449 (the softmax's loop is a third shorter; more copies of
+// its parts for special cases cost more than their branches: 510).  What bounds
+// it is the softmax's own latency: when the whole took 541 us, it took 275
+// without its arithmetic, 460 without the products, 446 without the widening and
+// as long as before without the exponentials alone.
 //
 // Two kinds of work: a sequence's own rows over what it sees (splits of a
 // unit's tiles are joined by the last CTA to arrive, in order), or, for a
