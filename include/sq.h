@@ -648,7 +648,8 @@ typedef struct {
  * out        device bf16 [T][hq][d];  lse  device float32 [T][hq], or NULL.
  * workspace  device scratch of sq_kv_attention_workspace_bytes() bytes, zero
  *            on first use and left zero where it must be by every call that
- *            finishes; one call at a time per workspace.  With less (or NULL)
+ *            finishes; one call at a time per workspace (calls of one stream,
+ *            from any host threads, come one after another).  With less (or NULL)
  *            the keys of a row are not split across CTAs and a shared prefix
  *            is read for every sequence: the same result but for the order of
  *            float32 sums, and slower.

@@ -48,6 +48,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "kv_attend.cuh"
 #include "kv_quant.cuh"
@@ -998,6 +999,17 @@ AttnPlan make_plan(int64_t T, int hq, int hkv, int B, int max_q, int64_t keys, i
   return p;
 }
 
+// Held over a call's launches, so that no other thread's call of the same stream comes between them: the
+// streaming kernel joins what the prefix pass right before it left in the workspace, and leaves out its
+// own first wait because that pass has made it.  Streams that share an entry only wait for one another's
+// launches; the default stream's two handles are one stream.
+std::mutex& launch_order(cudaStream_t stream) {
+  static std::mutex order[64];
+  uintptr_t h = reinterpret_cast<uintptr_t>(stream == nullptr ? cudaStreamLegacy : stream);
+  h ^= h >> 16;
+  return order[(h ^ (h >> 6)) & 63];
+}
+
 }  // namespace
 
 size_t attention_workspace_bytes(int64_t T, int hq, int hkv, int B, int max_q, int64_t keys,
@@ -1048,6 +1060,7 @@ sq_status run_attention(const void* q, int64_t q_stride, int64_t T, int hq,
     P.ex_o = reinterpret_cast<float*>(base + plan.ex_o);
     P.ex_ml = reinterpret_cast<float*>(base + plan.ex_ml);
   }
+  std::lock_guard<std::mutex> together(launch_order(stream));
   if (plan.tile || plan.shared) {
     const sq_status st = launch_tile(P, pages.bits, stream);
     if (st != SQ_OK) return st;
