@@ -80,6 +80,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
+// 1 / x of a power of two from 2^-126 to 2^126.
+__device__ __forceinline__ float reciprocal(float x) { return __uint_as_float(0x7F000000u - __float_as_uint(x)); }
+
 __device__ __forceinline__ uint32_t add_bits(uint32_t a, uint32_t b) {
   return h2_bits(__hadd2(bits_h2(a), bits_h2(b)));
 }
@@ -461,7 +464,11 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
     float ff[NT][2];                       // the scores' factor inside the exponential
 #pragma unroll
     for (int n = 0; n < NT; ++n) ff[n][0] = special ? 1.f : qf[n][0], ff[n][1] = special ? 1.f : qf[n][1];
-    float svr = 0.f, svi = 0.f;            // power of two at or above the value scales so far; 1 / svr
+    // 1 / a power of two above the value scales that the row has seen so far: a hidden key's, however
+    // large, takes no bits from the weights of a row
+    float svi[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) svi[n][0] = svi[n][1] = 8.507059e37f;  // 2^126
 
 #pragma unroll 1
     for (int seg = seg0; seg < 2; ++seg) {
@@ -526,6 +533,10 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 sc[gr][n][e] = fmaf(-kz[gr][e >> 1], qs[n][e & 1], sc[gr][n][e]) * sk[gr][e >> 1];
+          const float all = fmaxf(fmaxf(fabsf(sv[0][0]), fabsf(sv[0][1])), fmaxf(fabsf(sv[1][0]), fabsf(sv[1][1])));
+          float sva[NT][2];                // the largest value scale that the row sees of this lane's keys
+#pragma unroll
+          for (int n = 0; n < NT; ++n) sva[n][0] = sva[n][1] = plain ? all : 0.f;
           if (!plain) {
 #pragma unroll
             for (int gr = 0; gr < 2; ++gr) {
@@ -544,6 +555,7 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
                   const bool seen = dist >= 0 && (P.window == 0 || dist < P.window) &&
                                     local + 16 * gr + g + 8 * hf < limit && ((have >> gr) & 1u);
                   sc[gr][n][e] = seen ? x : -INFINITY;
+                  sva[n][c] = fmaxf(sva[n][c], seen ? fabsf(sv[gr][hf]) : 0.f);
                 }
               // rows behind the last key, and a group that is not there, hold anything
 #pragma unroll
@@ -560,30 +572,27 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
             for (int c = 0; c < 2; ++c) {
               mx[n][c] = fmaxf(fmaxf(sc[0][n][c], sc[0][n][2 + c]), fmaxf(sc[1][n][c], sc[1][n][2 + c])) *
                          ff[n][c];
-              raise |= mx[n][c] > m[n][c] + (kLift + kLazy);
+              raise |= mx[n][c] > m[n][c] + (kLift + kLazy) || sva[n][c] * svi[n][c] > 1.0f;
             }
-          const float sva = fmaxf(fmaxf(fabsf(sv[0][0]), fabsf(sv[0][1])), fmaxf(fabsf(sv[1][0]), fabsf(sv[1][1])));
-          raise |= sva > svr;
           if (__any_sync(0xffffffffu, raise)) {
-            float svmax = 0.f;             // infinities and NaN set none
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float a = fabsf(sv[j >> 1][j & 1]);
-              svmax = fmaxf(svmax, a <= 3.0e38f ? a : 0.f);
-            }
-#pragma unroll
-            for (int of = 4; of < 32; of <<= 1)
-              svmax = fmaxf(svmax, __shfl_xor_sync(0xffffffffu, svmax, of));
-            // a power of two at or above svmax, between 2^-126 and 2^126
-            const int e2 = max(1, min(253, static_cast<int>(__float_as_uint(svmax) >> 23) + 1));
-            const float nsv = fmaxf(svr, __uint_as_float(static_cast<uint32_t>(e2) << 23));
-            const float down = svr > 0.f ? svr / nsv : 0.f;
-            svr = nsv;
-            svi = 1.0f / nsv;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
+                float svmax = 0.f;         // infinities and NaN set none
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float a = fabsf(sv[j >> 1][j & 1]);
+                  svmax = fmaxf(svmax, a <= 3.0e38f && sc[j >> 1][n][2 * (j & 1) + c] != -INFINITY ? a : 0.f);
+                }
+#pragma unroll
+                for (int of = 4; of < 32; of <<= 1)
+                  svmax = fmaxf(svmax, __shfl_xor_sync(0xffffffffu, svmax, of));
+                // 1 / a power of two above svmax, between 2^-126 and 2^126
+                const int e2 = max(1, min(253, static_cast<int>(__float_as_uint(svmax) >> 23) + 1));
+                const float nsvi = fminf(svi[n][c], __uint_as_float(static_cast<uint32_t>(254 - e2) << 23));
+                const float down = nsvi * reciprocal(svi[n][c]);
+                svi[n][c] = nsvi;
                 float top = fmaxf(mx[n][c] - kLift, m[n][c]);
 #pragma unroll
                 for (int of = 4; of < 32; of <<= 1)
@@ -602,14 +611,13 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
           for (int gr = 0; gr < 2; ++gr) {
             // ---- weights, as fp16 pairs (high, low), to the B operand's layout
             uint32_t ph[NT][2], pl[NT][2];
-            const float wv[2] = {sv[gr][0] * svi, sv[gr][1] * svi};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               float p[4], w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 p[e] = ex2(fmaf(sc[gr][n][e], ff[n][e & 1], -m[n][e & 1]));
-                w[e] = p[e] * wv[e >> 1];
+                w[e] = p[e] * (sv[gr][e >> 1] * svi[n][e & 1]);
               }
               if (!plain) {                // no reference yet, or a hidden key's infinite scale
 #pragma unroll
@@ -700,12 +708,12 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
 
     // ---- the warps' results into shared memory.  Sums that large scales might carry past float32's end
     // before they are divided stand at 2^-40 of themselves, their reference 40 higher.
-    const float back = 16777216.0f * (svr >= 1.0f ? 9.094947e-13f : 1.0f);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int r = 8 * n + 2 * t + c;
+        const float svr = reciprocal(svi[n][c]), back = 16777216.0f * (svr >= 1.0f ? 9.094947e-13f : 1.0f);
 #pragma unroll
         for (int of = 4; of < 32; of <<= 1) {
           l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], of);

@@ -58,17 +58,29 @@ constexpr int OFF_V = OFF_K + 4 * PANEL;
 constexpr int OFF_SK = OFF_V + 4 * PANEL;  // float [4][KT]
 constexpr int OFF_SV = OFF_SK + 4 * KT * 4;
 constexpr int OFF_HID = OFF_SV + 4 * KT * 4;   // uint32 [4][8]: 4 words of hidden keys, 4 of flags
-constexpr int OFF_SVM = OFF_HID + 128;         // float [4][4]: largest value scale of 32 keys
-constexpr int OFF_BARS = OFF_SVM + 64;
+constexpr int OFF_SVE = OFF_HID + 128;         // float [4][4]: exponent above all value scales of 32 keys
+constexpr int OFF_RUN = OFF_SVE + 64;          // uint8 [4][KT][8]: the same, biased, of the 2^k keys from one on
+constexpr int OFF_BARS = OFF_RUN + 4 * KT * 8;
 constexpr int OFF_UNITS = OFF_BARS + 512;      // TileUnit [UNITS]
 constexpr int TILE_SMEM = OFF_UNITS + UNITS * 128 + 1024;
 constexpr uint32_t TILE_TMEM = 512;        // S [half][64 keys], O [half]
 constexpr uint32_t IDESC_S = idesc_f16(128, KT / 2, false, false);
-// A row's reference is its largest score so far less kTop (log2 units): weights reach 2^kTop and may
-// pass it by kSlack more before the sums are rescaled (which costs as much as the rest of a step;
-// with a slack of 1 it came in most of a prompt's steps).  fp16 then holds weights in full down to
-// 2^-(14 + kTop) of the largest and in fixed steps of 2^-(24 + kTop) below.
+// A row's reference is its largest score so far and the exponent of the largest value scale that it sees,
+// less kTop (log2 units): weights (times the values' scales) reach 2^kTop and may pass it by kSlack more
+// before the sums are rescaled (which costs as much as the rest of a step; with a slack of 1 it came in
+// most of a prompt's steps).  fp16 then holds weights in full down to 2^-(14 + kTop) of the largest and in
+// fixed steps of 2^-(24 + kTop) below.  A row's own scales count, since a hidden key's, however large, has
+// no business with its weights' precision; where a step shows a row a part of its keys, the exponent
+// is looked up by the run that it sees (prompts 464 us, against 452 with one exponent for all of a warp's
+// rows; 600 taken off the scores' registers, 530 in a loop over the keys).
 constexpr float kTop = 10.0f, kSlack = 5.0f;
+// Value scales are taken as they are while a step's largest is within 2^+-kEnds, else times a power of two
+// for all rows of the warp.  A row whose own are up to 2^kReach below that keeps its precision.
+constexpr float kEnds = 60.0f, kReach = 100.0f;
+// The sums of exponentials are held at 2^-40 of themselves: beside large scales, exponentials are up to
+// 2^(kTop + kSlack + kReach).
+constexpr float kDown = 9.094947e-13f;
+constexpr float kNone = -3.0e38f;          // the reference of a row that has seen no key
 constexpr uint32_t IDESC_O = idesc_f16(128, 128, false, true);
 
 struct TileBars {
@@ -294,6 +306,11 @@ __device__ __forceinline__ void mul2u(uint32_t& a, uint32_t& b, pair_t p) {
   b = __float_as_uint(r.y);
 }
 
+// 2^e for a whole e of -126 .. 127.
+__device__ __forceinline__ float power_of_two(float e) {
+  return __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(e)) << 23);
+}
+
 // The largest of three; NaN loses, as with fmaxf.
 __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
   float y;
@@ -493,7 +510,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
   float* s_sk = reinterpret_cast<float*>(smem + OFF_SK);
   float* s_sv = reinterpret_cast<float*>(smem + OFF_SV);
   uint32_t* s_hid = reinterpret_cast<uint32_t*>(smem + OFF_HID);
-  float* s_svm = reinterpret_cast<float*>(smem + OFF_SVM);
+  float* s_sve = reinterpret_cast<float*>(smem + OFF_SVE);
+  uint8_t* s_run = smem + OFF_RUN;
   TileBars& bar = *reinterpret_cast<TileBars*>(smem + OFF_BARS);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t spin = P.spin_limit;
@@ -558,9 +576,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
       const bool active = hf * HALF < rows;
       const int row = hf * HALF + r;
       // the rows of this thread's fragments: 16 bk + 8 i + g at index 2 bk + i
-      float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, l[4] = {0.f, 0.f, 0.f, 0.f};
-      float svr = 0.f;
-      bool far = true;
+      float m[4] = {kNone, kNone, kNone, kNone}, l[4] = {0.f, 0.f, 0.f, 0.f};
+      float sv_exp = -1000.f;                // value scales are taken times 2^-sv_exp; the first step sets it
+      bool far = false;                      // it is not 0
       if (active) {
         const int at = u.base + min(row, rows - 1), tok = at / P.G, head = u.h * P.G + at - tok * P.G;
         int row_pos = u.pos0 + tok;
@@ -728,41 +746,63 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
             }
           }
           // ---- references, and the sums rescaled where one has moved far
+          const float2 sve2 = *reinterpret_cast<const float2*>(s_sve + ring * 4 + 2 * b);
+          const float sve = fmaxf(sve2.x, sve2.y) - sv_exp, slack = kTop + kSlack - fmaxf(sve, -kReach);
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          bool raise = false;
+          bool raise = sve > kEnds;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
 #pragma unroll
             for (int c = 0; c < 8; ++c)
               mx[x] = max3(mx[x], v[x >> 1][4 * c + 2 * (x & 1)], v[x >> 1][4 * c + 2 * (x & 1) + 1]);
             mx[x] *= ff[x];
-            raise |= mx[x] > m[x] + (kTop + kSlack);
+            raise |= mx[x] - m[x] > slack;
           }
-          const float4 sm4 = *reinterpret_cast<const float4*>(s_svm + ring * 4);
-          const float svmax = fmaxf(fmaxf(sm4.x, sm4.y), fmaxf(sm4.z, sm4.w));
-          raise |= svmax > svr;
           if (__any_sync(0xffffffffu, raise)) {
-            // a power of two above svmax
-            const int e2 = max(1, min(253, static_cast<int>(__float_as_uint(svmax) >> 23) + 2));
-            const float nsv = fmaxf(svr, __uint_as_float(static_cast<uint32_t>(e2) << 23));
-            const float down = svr > 0.f ? svr / nsv : 0.f;
-            svr = nsv;
-            // exp2(s - m) / svr is one exponential while both its factors are far from float32's
-            // ends; otherwise 1 / svr is applied by itself
-            far = svr > 1.1529215e18f || svr < 8.6736174e-19f;          // 2^60, 2^-60
+            // lane t works out row t's reference
+            auto mine = [&](auto a0, auto a1, auto a2, auto a3) { return t & 2 ? (t & 1 ? a3 : a2) : (t & 1 ? a1 : a0); };
+            float seen = sve + sv_exp, shift = 0.f, low = 0.f;
+            if (sve > kEnds) {
+              // the scales' factor moves, and references with it as far as the sums of exponentials allow
+              const float to = fabsf(seen) > kEnds ? fminf(seen, 126.f) : 0.f;
+              shift = to - sv_exp;
+              sv_exp = to;
+              far = to != 0.f;
+              const float most = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
+              low = fminf(shift, 75.f - __log2f(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)))));
+            }
+            if (edge) {
+              // the keys that a row sees are a run
+              const int hi = mine(qpos[0], qpos[1], qpos[2], qpos[3]) - kpos + 1, lo = P.window > 0 ? hi - P.window : 0;
+              int e = 0;
+#pragma unroll
+              for (int w = 0; w < KT / 2; w += 32) {
+                const int a = max(lo - w, 0), len = min(hi - w, 32) - a;
+                if (len > 0) {
+                  const int k = 31 - __clz(len);
+                  const uint8_t* run = s_run + 8 * (ring * KT + key0 + w + a) + k;
+                  e = max(e, max(run[0], run[8 * (len - (1 << k))]));
+                }
+              }
+              seen = static_cast<float>(e - 126);
+            }
+            float top[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              top[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
+              top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
+            }
+            const float old = mine(m[0], m[1], m[2], m[3]);
+            const float now = fmaxf(old - low, mine(top[0], top[1], top[2], top[3]) + fmaxf(seen - sv_exp, -kReach) - kTop);
+            const float fa = ex2(old - now), down = ex2(-shift);
             float g4[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              float top = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-              const float nm = fmaxf(m[x], top - kTop);
-              const float fa = m[x] == -INFINITY ? 0.f : ex2(m[x] - nm);
-              m[x] = nm;
-              l[x] *= fa;
-              g4[x] = fa * down;
-              float off = nm == -INFINITY ? 0.f : -nm;
-              if (!far) off -= static_cast<float>(static_cast<int>(__float_as_uint(svr) >> 23) - 127);
-              mneg2[x] = pair_of(off, off);
+              m[x] = __shfl_sync(0xffffffffu, now, (lane & 28) + x);
+              g4[x] = __shfl_sync(0xffffffffu, fa, (lane & 28) + x);
+              l[x] *= g4[x];
+              g4[x] *= down;
+              mneg2[x] = pair_of(-m[x], -m[x]);
             }
             if (j > 0) {
               // the product of the step before; its barrier's phase before that was done when these
@@ -792,7 +832,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           uint32_t o[2][16];
           // (the common case is compiled by itself: branches inside cost it half its rate)
           auto weights = [&](auto careful) {
-            const float svi = !far ? 1.0f : svr > 0.f ? 1.0f / svr : 0.f;
+            const float svi = !far ? 1.0f : power_of_two(-sv_exp);
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               const pair_t sv = careful.value ? pair_mul(sv2[4 * c], pair_of(svi, svi)) : sv2[4 * c];
@@ -821,7 +861,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const float2 s2 = floats_of(sum[x]);
-            l[x] += (s2.x + s2.y) * (far ? 1.0f : svr);
+            l[x] = fmaf(s2.x + s2.y, kDown, l[x]);
           }
           tmem_st_wait();
           tc_fence_before();
@@ -847,11 +887,13 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
       }
       tiles += n;
       if (!ok) break;
-      // ---- out.  Partial sums that large scales might carry past float32's end stand at 2^-40 of
-      // themselves, their reference 40 higher.
+      // ---- out.  Partial results stay at 2^-40 of themselves, their reference 40 higher (large scales might
+      // carry them past float32's end), but where small scales might take them past its other end.
       const int pieces = u.pieces, slot = u.slot;
-      const bool split = pieces > 1 && !P.shared, live = row < rows, down40 = (split || P.shared) && svr >= 1.0f;
-      if (down40) mr += 40.0f, lr *= 9.094947e-13f;
+      const bool split = pieces > 1 && !P.shared, live = row < rows;
+      const float svr = power_of_two(fmaxf(sv_exp, -126.f));
+      mr = lr == 0.f ? -INFINITY : mr + 40.0f;
+      if ((split || P.shared) && sv_exp < 0.f) mr -= 40.0f, lr *= 1.0f / kDown;
       const int at = u.base + min(row, rows - 1), tok = at / P.G, head = u.h * P.G + at - tok * P.G;
       const int64_t out_row = static_cast<int64_t>(u.row0 + tok) * P.hq + head;
       float* part_o = nullptr;               // partial results, and this row's place in them
@@ -876,7 +918,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
       if (active) {
         // through this half's queries, which nothing reads any more, so that 16 lanes store a row's
         // whole lines
-        const float inv = part_o ? (down40 ? 9.094947e-13f : 1.0f) : lr == 0.f ? 0.f : 1.0f / lr;
+        // (a result's 2^-40 in two parts: neither factor leaves float32's range)
+        const float inv = part_o ? (sv_exp < 0.f ? 1.0f : kDown) : lr == 0.f ? 0.f : 9.5367432e-07f / lr;
+        const float fac = part_o ? svr : svr * 9.5367432e-07f;
         uint8_t* stage = smem + OFF_Q + hf * 2 * PANEL;
         const int lane_row = part_o ? static_cast<int>(part_row) : static_cast<int>(out_row);
         const int passes = part_o ? 2 : 1;
@@ -896,7 +940,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
 #pragma unroll
               for (int d = 0; d < 8; ++d) {
                 const float o = __uint_as_float(v[8 * c8 + place8<BITS>(d)]);
-                y[d] = n > 0 && lr != 0.f ? o * inv * svr : 0.f;
+                y[d] = n > 0 && lr != 0.f ? o * inv * fac : 0.f;
               }
               if (part_o) {
                 const int at = 8 * (c & 1) + 2 * c8;
@@ -1090,10 +1134,20 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
         s_sv[ring * KT + wrow + lane] = gone ? 0.f : sv;
         const float a = gone ? 0.f : fabsf(sv);
         const bool fine = a <= 3.0e38f;
-        const uint32_t svm = __reduce_max_sync(0xffffffffu, fine ? __float_as_uint(a) : 0u);
+        // exponents: the largest of the 2^k value scales from this lane's on, a byte for each k of 0 .. 5
+        // (infinities and NaN count as zeros)
+        uint32_t top = fine ? __float_as_uint(a) >> 23 : 0u;
+        uint32_t run[2] = {top, 0u};
+#pragma unroll
+        for (int k = 1; k < 6; ++k) {
+          const uint32_t next = __shfl_down_sync(0xffffffffu, top, 1 << (k - 1));
+          if (lane + (1 << (k - 1)) < 32) top = max(top, next);
+          run[k >> 2] |= top << (8 * (k & 3));
+        }
+        *reinterpret_cast<uint2*>(s_run + 8 * (ring * KT + wrow + lane)) = make_uint2(run[0], run[1]);
         const uint32_t hid = __ballot_sync(0xffffffffu, gone), bad = __ballot_sync(0xffffffffu, !fine);
         if (lane == 0) {
-          s_svm[ring * 4 + pw] = __uint_as_float(svm);
+          s_sve[ring * 4 + pw] = static_cast<float>(static_cast<int>(top) - 126);
           s_hid[ring * 8 + pw] = hid;
           s_hid[ring * 8 + 4 + pw] = (hid != 0 ? 1u : 0u) | (bad != 0 ? 2u : 0u);
         }

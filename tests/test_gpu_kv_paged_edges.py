@@ -8,7 +8,7 @@ import torch
 
 import rotation_ptq_b200 as sq
 from tests import paged as G
-from tests.test_gpu_kv_paged import attend, bf16, cu, pages_of, problems_of_all_kinds
+from tests.test_gpu_kv_paged import STREAM_EPS, TILE_EPS, TILE_STEP, attend, bf16, cu, pages_of, problems_of_all_kinds
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +52,38 @@ def test_host_threads_share_a_stream():
         n = sum(probs[i].new)
         assert torch.equal(out[:n], first[i][:n])
     assert sq.device_status() == 0
+
+
+def scale_key(prob, pos, factor):
+    """Multiplies the value scale of sequence 0's key at `pos`; prob.values keeps what it was."""
+    at = prob.pool.table[0, pos // prob.pool.page], slice(None), pos % prob.pool.page
+    prob.pool.arrays["v_scale"][at] *= np.float32(factor)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("factor", [1e9, 1e20, 1e30])
+@pytest.mark.parametrize("new,own,window,pos", [
+    (6, 80, 0, 79),                                 # streaming kernel: a later token's key
+    (6, 80, 10, 65),                                # one that only the first token still sees
+    (1, 300, 100, 196),                             # one that the window has left behind, beside visible keys
+    (64, 200, 0, 199),                              # tile kernel: the same three
+    (64, 200, 10, 130),
+    (64, 400, 100, 236),
+])
+def test_hidden_value_scales_take_no_precision(new, own, window, pos, factor, bits):
+    """A key's value scale, however large, is no business of the rows from which it is hidden: their results
+    keep the bounds of what they see."""
+    prob = G.Attention(61, [new], [own], 4, 1, 16, bits, window=window)
+    ref = prob.reference()
+    tile = new * 4 > 32
+    b_out, b_lse = prob.bounds(ref, *((TILE_EPS, TILE_STEP) if tile else (STREAM_EPS,)))
+    scale_key(prob, pos, factor)
+    out, lse = attend(prob)
+    dist = own - new + np.arange(new) - pos
+    blind = (dist < 0) | ((dist >= window) if window else False)
+    assert blind.any()
+    o, m = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    err = np.abs(o - ref[0])[blind] / b_out[blind]
+    assert (err <= 1).all(), "out: %.3g times its bound" % err.max()
+    assert (np.abs(m - ref[1]) <= b_lse).all()
+    assert np.isfinite(o).all() and sq.device_status() == 0
