@@ -635,11 +635,14 @@ typedef struct {
  * zeros and lse -inf.  Weights of the softmax are held to 22 bits for sequences
  * of up to 32 rows (new tokens x hq / hkv), to 11 bits (fp16) for more and over a
  * prefix that is read once for the batch; times their values' scales they are
- * held in steps of no less than 2^-37 and 2^-32 of the row's largest weight times
+ * held in steps no coarser than 2^-37 and 2^-32 of the row's largest weight times
  * the largest scale that it sees.
  *
  * q          device bf16 [T][hq][d] (q_out of the append), heads contiguous,
- *            q_stride elements between tokens (a multiple of 8).
+ *            q_stride elements between tokens (a multiple of 8).  Any finite
+ *            size, over key scales of up to 2^96; where scores are so large that
+ *            float32 holds them in steps of many, a row is an average of its
+ *            largest keys' values.
  * lengths    device int32 [B]: cached tokens, the new ones included.  A
  *            sequence whose length is out of range (of its table) is reported
  *            and gets zeros; one whose rows do not lie in the batch is

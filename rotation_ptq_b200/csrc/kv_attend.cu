@@ -128,7 +128,8 @@ struct Stream {
   }
 
   // Query fragments of the unit's rows, and each of this thread's two columns'
-  // factor (log2 units, or plain when the scores are capped).
+  // factor (log2 units, or plain when the scores are capped), 2^24 aside: a
+  // row near bf16's end would carry the product past float32's.
   static __device__ __forceinline__ void load_q(const AttnParams& P, const Unit& u, int g, int t,
                                                 uint32_t (&qb)[NT][8][2], float (&qf)[NT][2],
                                                 float (&qs)[NT][2]) {
@@ -163,9 +164,10 @@ struct Stream {
       float f = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
       const float inv = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
       // a factor >= 0 lets the maximum be taken before it is applied
-      float mine = inv * 16777216.0f * P.scale * (P.cap > 0.f ? 1.0f / P.cap : kLog2e);
+      float mine = inv * P.scale * (P.cap > 0.f ? 1.0f / P.cap : kLog2e);
       if (mine < 0.f) mine = -mine, f = -f;
       if (mine == 0.f) mine = 1.f, f = 0.f;
+      mine = fminf(mine, 3.0e38f);         // times a score of zero, an infinity would be NaN
       // 4-bit codes of the second register of a pair are 16 n 2^-24
       const float fb = BITS == 4 ? f * 0.0625f : f;
       float sum = 0.f;
@@ -461,9 +463,18 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
       l[n][0] = l[n][1] = 0.f;
     }
     const bool special = P.cap > 0.f || P.slopes != nullptr;
-    float ff[NT][2];                       // the scores' factor inside the exponential
+    // The rows' factors wait for the exponential's fused multiply-add, unless the scores are capped or
+    // sloped, so large (kPlain) that the multiply-add's own rounding would tell its result from the
+    // maximum's, or a row's factor leaves float32: then they are applied to the scores.
+    bool factored = special;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) ff[n][0] = special ? 1.f : qf[n][0], ff[n][1] = special ? 1.f : qf[n][1];
+    for (int n = 0; n < NT; ++n) factored = factored || qf[n][0] > 1.0e30f || qf[n][1] > 1.0e30f;
+    factored = __any_sync(0xffffffffu, factored);
+    float ff[NT][2];                       // the factor inside the exponential
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) ff[n][e] = factored ? 1.f : qf[n][e] * 16777216.0f;
     // 1 / a power of two above the value scales that the row has seen so far: a hidden key's, however
     // large, takes no bits from the weights of a row
     float svi[NT][2];
@@ -533,6 +544,15 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 sc[gr][n][e] = fmaf(-kz[gr][e >> 1], qs[n][e & 1], sc[gr][n][e]) * sk[gr][e >> 1];
+          auto apply = [&]() {
+#pragma unroll
+            for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[gr][n][e] = sc[gr][n][e] * qf[n][e & 1] * 16777216.0f;
+          };
+          if (factored) apply();
           const float all = fmaxf(fmaxf(fabsf(sv[0][0]), fabsf(sv[0][1])), fmaxf(fabsf(sv[1][0]), fabsf(sv[1][1])));
           float sva[NT][2];                // the largest value scale that the row sees of this lane's keys
 #pragma unroll
@@ -548,7 +568,6 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
                   float x = sc[gr][n][e];
                   const int dist = qpos[n][c] - (kpos + 16 * gr + g + 8 * hf);
                   if (special) {
-                    x *= qf[n][c];
                     if (P.cap > 0.f) x = P.cap * kLog2e * tanh_score(x);
                     x = fmaf(-slope[n][c], static_cast<float>(dist), x);
                   }
@@ -572,9 +591,10 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
             for (int c = 0; c < 2; ++c) {
               mx[n][c] = fmaxf(fmaxf(sc[0][n][c], sc[0][n][2 + c]), fmaxf(sc[1][n][c], sc[1][n][2 + c])) *
                          ff[n][c];
-              raise |= mx[n][c] > m[n][c] + (kLift + kLazy) || sva[n][c] * svi[n][c] > 1.0f;
+              raise |= mx[n][c] - m[n][c] > kLift + kLazy || sva[n][c] * svi[n][c] > 1.0f;
             }
           if (__any_sync(0xffffffffu, raise)) {
+            bool large = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -593,10 +613,13 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
                 const float nsvi = fminf(svi[n][c], __uint_as_float(static_cast<uint32_t>(254 - e2) << 23));
                 const float down = nsvi * reciprocal(svi[n][c]);
                 svi[n][c] = nsvi;
-                float top = fmaxf(mx[n][c] - kLift, m[n][c]);
+                float top = mx[n][c];
 #pragma unroll
                 for (int of = 4; of < 32; of <<= 1)
                   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, of));
+                // (float32's steps may be wider than the lift)
+                top = fmaxf(top - (top - kLift) > kLift + kLazy ? top : top - kLift, m[n][c]);
+                large |= top > kPlain || (top < -kPlain && top > -INFINITY);
                 const float f = m[n][c] == -INFINITY ? 0.f : ex2(m[n][c] - top);
                 m[n][c] = top;
                 l[n][c] *= f;
@@ -606,6 +629,12 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
                   o[n][i8][2 + c] *= f * down;
                 }
               }
+            if (!factored && __any_sync(0xffffffffu, large)) {
+              apply();
+              factored = true;
+#pragma unroll
+              for (int n = 0; n < NT; ++n) ff[n][0] = ff[n][1] = 1.f;
+            }
           }
 #pragma unroll
           for (int gr = 0; gr < 2; ++gr) {

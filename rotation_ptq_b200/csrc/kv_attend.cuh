@@ -14,6 +14,9 @@ namespace paged {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// From scores of 2^22 (log2 units: float32 steps of a half) on, the exponential's argument is rounded like the
+// maximum's, in two steps: a fused multiply-add would tell them apart by more than weights have room for.
+constexpr float kPlain = 4194304.0f;
 constexpr int TILE = 128;                  // keys per CTA step of the streaming kernel
 
 struct AttnParams {

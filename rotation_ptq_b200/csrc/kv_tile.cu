@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
       // the rows of this thread's fragments: 16 bk + 8 i + g at index 2 bk + i
       float m[4] = {kNone, kNone, kNone, kNone}, l[4] = {0.f, 0.f, 0.f, 0.f};
       float sv_exp = -1000.f;                // value scales are taken times 2^-sv_exp; the first step sets it
-      bool far = false;                      // it is not 0
+      bool far = false;                      // it is not 0, or a row's scores are past kPlain
       if (active) {
         const int at = u.base + min(row, rows - 1), tok = at / P.G, head = u.h * P.G + at - tok * P.G;
         int row_pos = u.pos0 + tok;
@@ -623,6 +623,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           // a factor >= 0 lets the maximum be taken before it is applied
           if (f < 0.f) f = -f, qf = -qf;
           if (f == 0.f) f = 1.f, qf = 0.f;
+          f = fminf(f, 3.0e38f);               // times a score of zero, an infinity would be NaN
           const float both = __shfl_sync(0xffffffffu, f, (lane & 1) << 4);   // of row 2 i + (lane & 1)
           if (lane >> 1 == i) row_f = both;
           float v[8];
@@ -755,7 +756,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
 #pragma unroll
             for (int c = 0; c < 8; ++c)
               mx[x] = max3(mx[x], v[x >> 1][4 * c + 2 * (x & 1)], v[x >> 1][4 * c + 2 * (x & 1) + 1]);
-            mx[x] *= ff[x];
+            mx[x] = __fmul_rn(mx[x], ff[x]);
             raise |= mx[x] - m[x] > slack;
           }
           if (__any_sync(0xffffffffu, raise)) {
@@ -767,7 +768,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
               const float to = fabsf(seen) > kEnds ? fminf(seen, 126.f) : 0.f;
               shift = to - sv_exp;
               sv_exp = to;
-              far = to != 0.f;
               const float most = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
               low = fminf(shift, 75.f - __log2f(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)))));
             }
@@ -795,6 +795,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
             const float old = mine(m[0], m[1], m[2], m[3]);
             const float now = fmaxf(old - low, mine(top[0], top[1], top[2], top[3]) + fmaxf(seen - sv_exp, -kReach) - kTop);
             const float fa = ex2(old - now), down = ex2(-shift);
+            far = sv_exp != 0.f || __any_sync(0xffffffffu, fabsf(now) > kPlain && now > kNone);
             float g4[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -839,7 +840,12 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 const int at = 4 * c + 2 * (x & 1);
-                const float2 y = floats_of(pair_fma(pair_of(v[x >> 1][at], v[x >> 1][at + 1]), ff2[x], mneg2[x]));
+                float2 y;
+                if (careful.value)             // (never fused by the compiler, which a mul and an add of pairs were)
+                  y = make_float2(__fadd_rn(__fmul_rn(__uint_as_float(v[x >> 1][at]), ff[x]), -m[x]),
+                                  __fadd_rn(__fmul_rn(__uint_as_float(v[x >> 1][at + 1]), ff[x]), -m[x]));
+                else
+                  y = floats_of(pair_fma(pair_of(v[x >> 1][at], v[x >> 1][at + 1]), ff2[x], mneg2[x]));
                 const float2 e = make_float2(ex2(y.x), ex2(y.y));
                 const pair_t a = pair_of(e.x, e.y);
                 sum[x] = pair_add(sum[x], a);

@@ -8,7 +8,7 @@ import torch
 
 import rotation_ptq_b200 as sq
 from tests import paged as G
-from tests.test_gpu_kv_paged import STREAM_EPS, TILE_EPS, TILE_STEP, attend, bf16, cu, pages_of, problems_of_all_kinds
+from tests.test_gpu_kv_paged import STREAM_EPS, TILE_EPS, TILE_STEP, attend, bf16, check, cu, pages_of, problems_of_all_kinds
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +87,33 @@ def test_hidden_value_scales_take_no_precision(new, own, window, pos, factor, bi
     assert (err <= 1).all(), "out: %.3g times its bound" % err.max()
     assert (np.abs(m - ref[1]) <= b_lse).all()
     assert np.isfinite(o).all() and sq.device_status() == 0
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("rule", [{}, dict(softcap=20.0), dict(slopes=True), dict(scale=-0.1), dict(window=20)])
+@pytest.mark.parametrize("q_size,k_size", [(3e36, 3e-37), (1e38, 1e-37), (1e-36, 1e30), (1e5, 1e-36)])
+@pytest.mark.parametrize("new", [1, 3, 64])
+def test_queries_at_the_ends(new, q_size, k_size, rule, bits):
+    """Queries up to bf16's end over keys that leave their scores moderate."""
+    prob = G.Attention(62, [new], [200], 4, 1, 16, bits, q_size=q_size, k_size=k_size, **rule)
+    prob.q = G.round_bf16(np.clip(prob.q, -3.3e38, 3.3e38))      # (the oracle gets what the kernel gets)
+    check(prob, *attend(prob))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("rule", [{}, dict(slopes=True), dict(scale=-0.1), dict(window=20)])
+@pytest.mark.parametrize("q_size,k_size", [(1e4, 1e3), (1e4, 1e5), (1e9, 1e6), (1e20, 1e10), (1.0, 1e28)])
+@pytest.mark.parametrize("new", [1, 3, 64])
+def test_scores_far_past_the_exponential(new, q_size, k_size, rule, bits):
+    """Scores so large that float32 holds them in steps of many: a row is still an average of its visible
+    values, and its log sum is its largest score's."""
+    prob = G.Attention(63, [new], [200], 4, 1, 16, bits, q_size=q_size, k_size=k_size, **rule)
+    out, lse = attend(prob)
+    check(prob, out, lse)
+    o = out.double().cpu().numpy()
+    for i in range(new):
+        at = 200 - new + i
+        seen = prob.values["v", 0][max(0, at + 1 - (rule.get("window") or 200)):at + 1, 0]
+        # weights (11 bits) and their sum's rounding, and bf16's
+        slack = (2.0 ** -8 + 2.0 ** -9) * np.abs(seen).max()
+        assert (o[i] <= seen.max(0) + slack).all() and (o[i] >= seen.min(0) - slack).all()
