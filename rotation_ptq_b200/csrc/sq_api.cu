@@ -395,7 +395,7 @@ sq_status sq_kv_paged_append(const void* q, const void* k, const void* v, int64_
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
       !aligned4(block_table) || !aligned4(cu_seqlens) || !aligned4(cached) ||
       !aligned16(rope_cos) || !aligned16(rope_sin) || !aligned16(q_norm) || !aligned16(k_norm)) {
-    set_error("device pointers must be 16-byte aligned (int32 arrays, slopes and lse: 4-byte)");
+    set_error("device pointers must be 16-byte aligned (int32 arrays: 4-byte)");
     return SQ_ERR_MISALIGNED;
   }
   st = precheck_device();
@@ -419,7 +419,7 @@ sq_status sq_kv_paged_dequant(const sq_kv_pages* pages, const int32_t* block_tab
   }
   if (!aligned4(block_table) || !aligned4(cu_seqlens) || !aligned4(cached) ||
       !aligned16(k_out) || !aligned16(v_out)) {
-    set_error("device pointers must be 16-byte aligned (int32 arrays, slopes and lse: 4-byte)");
+    set_error("device pointers must be 16-byte aligned (int32 arrays: 4-byte)");
     return SQ_ERR_MISALIGNED;
   }
   st = precheck_device();
@@ -552,7 +552,7 @@ sq_status sq_w4a4_linear(const uint8_t* a_q, const float* a_scale, const uint8_t
   }
   if (!aligned16(a_q) || !aligned16(a_scale) || !aligned16(w_q) || !aligned16(w_scale) ||
       !aligned16(out) || (workspace && !aligned16(workspace))) {
-    set_error("device pointers must be 16-byte aligned (int32 arrays, slopes and lse: 4-byte)");
+    set_error("device pointers must be 16-byte aligned");
     return SQ_ERR_MISALIGNED;
   }
   sq_status st = precheck_device();
@@ -587,7 +587,7 @@ sq_status sq_w4a8_linear(const int8_t* a_q, const float* a_scale, const uint8_t*
   }
   if (!aligned16(a_q) || !aligned16(a_scale) || !aligned16(w_q) || !aligned16(w_scale) ||
       !aligned16(out) || (workspace && !aligned16(workspace))) {
-    set_error("device pointers must be 16-byte aligned (int32 arrays, slopes and lse: 4-byte)");
+    set_error("device pointers must be 16-byte aligned");
     return SQ_ERR_MISALIGNED;
   }
   sq_status st = precheck_device();
@@ -632,7 +632,7 @@ static sq_status kv_rotate_quant(const void* q, const void* k, const void* v, in
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
       !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale) ||
       !aligned16(pos) || (rope_cos && (!aligned16(rope_cos) || !aligned16(rope_sin)))) {
-    set_error("device pointers must be 16-byte aligned (int32 arrays, slopes and lse: 4-byte)");
+    set_error("device pointers must be 16-byte aligned");
     return SQ_ERR_MISALIGNED;
   }
   sq_status st = precheck_device();
@@ -678,7 +678,7 @@ static sq_status kv_dequant(const uint8_t* cache, const float* scale, const uint
     return SQ_ERR_INVALID_ARG;
   }
   if (!aligned16(cache) || !aligned16(scale) || !aligned16(out_bf16)) {
-    set_error("device pointers must be 16-byte aligned (int32 arrays, slopes and lse: 4-byte)");
+    set_error("device pointers must be 16-byte aligned");
     return SQ_ERR_MISALIGNED;
   }
   sq_status st = precheck_device();
@@ -821,7 +821,7 @@ sq_status sq_cayley_update(const double* R, const double* G, double alpha, int n
   }
   if (!aligned16(R) || !aligned16(G) || !aligned16(R_out) || !aligned16(workspace) ||
       (R_out_f32 && !aligned16(R_out_f32))) {
-    set_error("device pointers must be 16-byte aligned (int32 arrays, slopes and lse: 4-byte)");
+    set_error("device pointers must be 16-byte aligned");
     return SQ_ERR_MISALIGNED;
   }
   sq_status st = precheck_device();
@@ -879,7 +879,7 @@ sq_status sq_rope_tables(double theta, int max_pos, int d, float* cos, float* si
     return SQ_ERR_INVALID_ARG;
   }
   if (!aligned16(cos) || !aligned16(sin)) {
-    set_error("device pointers must be 16-byte aligned (int32 arrays, slopes and lse: 4-byte)");
+    set_error("device pointers must be 16-byte aligned");
     return SQ_ERR_MISALIGNED;
   }
   sq_status st = precheck_device();
