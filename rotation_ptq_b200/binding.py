@@ -510,6 +510,7 @@ def rope_tables(theta: float, max_pos: int, d: int = 128, device=None):
     device = torch.device("cuda") if device is None else torch.device(device)
     cos = torch.empty((max_pos, d // 2), dtype=torch.float32, device=device)
     sin = torch.empty_like(cos)
+    _need_cuda(cos)
     st = lib.sq_rope_tables(float(theta), max_pos, d, cos.data_ptr(), sin.data_ptr(),
                             _stream(cos))
     _check(st, "sq_rope_tables")
