@@ -649,7 +649,8 @@ typedef struct {
  *            reported and left out.  Rows of a page that is out of range
  *            are reported and taken as hidden.
  * max_q      the most new tokens that any sequence has.  It picks the kernel:
- *            results hold for longer sequences too, at a lower speed.
+ *            results hold for longer sequences too, at a lower speed.  0 says
+ *            that no sequence has any: nothing is written.
  * out        device bf16 [T][hq][d];  lse  device float32 [T][hq], or NULL.
  * workspace  device scratch of sq_kv_attention_workspace_bytes() bytes, zero
  *            on first use and left zero where it must be by every call that

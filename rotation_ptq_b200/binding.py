@@ -159,6 +159,7 @@ SQ_ERR_TIMEOUT = 5
 
 
 _Tensor = torch.Tensor
+_I32_MAX = 2 ** 31 - 1
 
 
 def _expect(t, name, dtype, shape):
@@ -692,6 +693,14 @@ def _heads(t, name, heads=None):
     return s[0]
 
 
+def _whole(v, name, most):
+    """A whole number from 0 to `most`: ctypes would wrap a larger one to fit without a word."""
+    n = int(v)
+    if n != v or not 0 <= n <= most:
+        raise ValueError("%s must be a whole number from 0 to %d, got %s" % (name, most, v))
+    return n
+
+
 def _expect_batch(pages, block_table, cu_seqlens, lengths, lname):
     if not isinstance(pages, KVPages):
         raise TypeError("pages must be a KVPages")
@@ -783,7 +792,7 @@ def kv_paged_dequant(pages: KVPages, block_table: torch.Tensor, cu_seqlens: torc
     behind cu_seqlens[B] are not written.
     """
     B, width = _expect_batch(pages, block_table, cu_seqlens, cached, "cached")
-    shape = (int(num_tokens), pages.hkv, 128)
+    shape = (_whole(num_tokens, "num_tokens", _I32_MAX), pages.hkv, 128)
     for t, nm in ((k_out, "k_out"), (v_out, "v_out")):
         if t is not None:
             _expect(t, nm, torch.bfloat16, shape)
@@ -809,8 +818,9 @@ def kv_attention_workspace_bytes(T: int, hq: int, pages: KVPages, B: int, table_
                                  max_q: int, prefix_len: int = 0) -> int:
     """Scratch bytes that let the paged attention calls split keys across CTAs
     (and read a shared prefix once)."""
-    return int(lib.sq_kv_attention_workspace_bytes(int(T), int(hq), pages._ref, int(B),
-                                                   int(table_width), int(max_q), int(prefix_len)))
+    return int(lib.sq_kv_attention_workspace_bytes(
+        int(T), _whole(hq, "hq", _I32_MAX), pages._ref, _whole(B, "B", _I32_MAX),
+        _whole(table_width, "table_width", _I32_MAX), _whole(max_q, "max_q", _I32_MAX), int(prefix_len)))
 
 
 def kv_paged_attention(q: torch.Tensor, pages: KVPages, block_table: torch.Tensor,
@@ -822,7 +832,8 @@ def kv_paged_attention(q: torch.Tensor, pages: KVPages, block_table: torch.Tenso
     (``sq_kv_paged_attention``).
 
     q bf16 [T, hq, 128] (what kv_paged_append returned); lengths int32 [B], the
-    cached tokens with the new ones; max_q, the most new tokens of a sequence.
+    cached tokens with the new ones; max_q, the most new tokens of a sequence
+    (0: none has any, and nothing is written).
     scale defaults to 1/sqrt(128); softcap caps scores by a tanh; window hides
     keys that far back; slopes (float32 [hq]) subtract slope x distance.
     Returns bf16 [T, hq, 128]; lse (float32 [T, hq]), where given, is written.
@@ -874,6 +885,7 @@ def _attention_workspace(device, stream, need):
 def _kv_attention(q, pages, prefix_table, prefix_len, block_table, cu_seqlens, lengths, max_q,
                   scale, softcap, window, slopes, out, lse, workspace):
     B, width = _expect_batch(pages, block_table, cu_seqlens, lengths, "lengths")
+    max_q, window = _whole(max_q, "max_q", _I32_MAX), _whole(window, "window", 1 << 30)
     stride = _heads(q, "q")
     T, hq = q.shape[0], q.shape[1]
     if hq % pages.hkv or hq > 256:
@@ -890,9 +902,8 @@ def _kv_attention(q, pages, prefix_table, prefix_len, block_table, cu_seqlens, l
     _need_cuda(q, pages.k_codes)
     if out is None:
         out = torch.empty((T, hq, 128), dtype=torch.bfloat16, device=q.device)
-    rule = _ScoreRule(128 ** -0.5 if scale is None else float(scale), float(softcap), int(window),
+    rule = _ScoreRule(128 ** -0.5 if scale is None else float(scale), float(softcap), window,
                       _ptr(slopes))
-    max_q = int(max_q)
     stream = _stream(q)
     back = _enter(q.get_device())
     try:
