@@ -589,7 +589,7 @@ typedef struct {
  *            Positions from max_pos on are out of range.
  * rot        rotated channels: a multiple of 16, 16..128 (read with tables).
  * q_norm, k_norm  device float32 [d], or NULL.  eps >= 0.
- * q_out      device bf16 [T][hq][d] (written; may not overlap q).
+ * q_out      device bf16 [T][hq][d] (written; may not overlap q, k or v: refused).
  * A token whose sequence, position or page is out of range is reported and
  * written nowhere.  The positions of one call must lie in different rows:
  * of two tokens sent to the same row (a page in two sequences' tables at the

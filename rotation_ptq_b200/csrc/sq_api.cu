@@ -360,6 +360,13 @@ static bool stride_ok(int64_t stride, int heads) {
   return stride >= static_cast<int64_t>(heads) * 128 && stride % 8 == 0 && stride < (1LL << 31);
 }
 
+// Whether rows of `heads` heads, `stride` elements apart, reach into the bytes from lo to hi.
+static bool rows_reach(const void* rows, int64_t stride, int64_t T, int heads, uintptr_t lo,
+                       uintptr_t hi) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(rows);
+  return at < hi && lo < at + static_cast<uintptr_t>((T - 1) * stride + heads * 128) * 2;
+}
+
 sq_status sq_kv_paged_append(const void* q, const void* k, const void* v, int64_t q_stride,
                              int64_t k_stride, int64_t v_stride, int64_t T, int hq,
                              const sq_kv_pages* pages, const int32_t* block_table,
@@ -397,6 +404,13 @@ sq_status sq_kv_paged_append(const void* q, const void* k, const void* v, int64_
       !aligned16(rope_cos) || !aligned16(rope_sin) || !aligned16(q_norm) || !aligned16(k_norm)) {
     set_error("device pointers must be 16-byte aligned (int32 arrays: 4-byte)");
     return SQ_ERR_MISALIGNED;
+  }
+  // a token's query heads are written while other heads' values are still read
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(q_out), hi = lo + static_cast<uintptr_t>(T) * hq * 256;
+  if (rows_reach(q, q_stride, T, hq, lo, hi) || rows_reach(k, k_stride, T, pages->hkv, lo, hi) ||
+      rows_reach(v, v_stride, T, pages->hkv, lo, hi)) {
+    set_error("q_out may not overlap q, k or v");
+    return SQ_ERR_INVALID_ARG;
   }
   st = precheck_device();
   if (st != SQ_OK) return st;
