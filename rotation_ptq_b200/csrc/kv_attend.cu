@@ -47,6 +47,7 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -987,21 +988,25 @@ constexpr int kFewRows = 32;
 // come to kSharedTiles an SM.  4-bit, us, streaming against shared: 16 single tokens behind 4096 keys
 // 38 / 42, behind 10000 67 / 52; 32 behind 2000 42 / 43, behind 4096 60 / 44; 64 behind 700 44 / 55,
 // behind 2000 65 / 55; 5 new tokens each, 6 sequences behind 2000 39 / 47, 32 behind 2000 108 / 89.
+// Under a window only the prefix's last keys count: either side reads no others.
 constexpr int kSharedRows = 128;
 constexpr int kSharedTiles = 30;
 constexpr size_t kSharedBytes = size_t{1} << 30;          // of partial results: larger batches stream
 constexpr int kTileRows = 256;
 constexpr size_t kPartFloats = static_cast<size_t>(kTileRows) * (D + 2);
 
+// share: whether a shared prefix may have a pass of its own (without: a workspace's size where a window rules it out).
 AttnPlan make_plan(int64_t T, int hq, int hkv, int B, int max_q, int64_t keys, int prefix_len,
-                   int bits, bool have_ws) {
+                   int window, int bits, bool have_ws, bool share = true) {
   AttnPlan p{};
   const int64_t G = hq / hkv, rows = G * max_q;
   const int sms = host::num_sms();
   p.kind = rows <= 4 ? 0 : rows <= 8 ? 1 : 2;
   const int64_t per_unit = stream_of(bits, p.kind).rows;
-  p.shared = have_ws && B > 1 && prefix_len > 0 && rows <= kSharedRows &&
-             B * ((rows + per_unit - 1) / per_unit) * hkv * ((prefix_len + TILE - 1) / TILE) >=
+  // rows of the prefix that a sequence without keys of its own sees under the window
+  const int64_t seen = window > 0 ? std::min<int64_t>(prefix_len, static_cast<int64_t>(window) + max_q) : prefix_len;
+  p.shared = share && have_ws && B > 1 && prefix_len > 0 && rows <= kSharedRows &&
+             B * ((rows + per_unit - 1) / per_unit) * hkv * ((seen + TILE - 1) / TILE) >=
                  static_cast<int64_t>(kSharedTiles) * sms &&
              static_cast<size_t>(T) * hq * D * 4 <= kSharedBytes;
   p.tile = !p.shared && rows > kFewRows;
@@ -1016,7 +1021,7 @@ AttnPlan make_plan(int64_t T, int hq, int hkv, int B, int max_q, int64_t keys, i
   if (p.stream)
     p.part = take(static_cast<size_t>(stream_grid(bits, p.kind)) * 2 * stream_of(bits, p.kind).rows * (D + 2) * 4);
   if (p.shared) {
-    const int64_t units = (T * G + kTileRows - 1) / kTileRows * hkv, tiles = (prefix_len + 127) / 128;
+    const int64_t units = (T * G + kTileRows - 1) / kTileRows * hkv, tiles = (seen + 127) / 128;
     int64_t s = sms / units;
     if (s > (tiles + 1) / 2) s = (tiles + 1) / 2;
     p.tile_split = static_cast<int>(s < 1 ? 1 : s);
@@ -1051,7 +1056,9 @@ std::mutex& launch_order(cudaStream_t stream) {
 
 size_t attention_workspace_bytes(int64_t T, int hq, int hkv, int B, int max_q, int64_t keys,
                                  int prefix_len, int bits) {
-  return make_plan(T, hq, hkv, B, max_q, keys, prefix_len, bits, true).bytes;
+  // for any window
+  return std::max(make_plan(T, hq, hkv, B, max_q, keys, prefix_len, 0, bits, true).bytes,
+                  make_plan(T, hq, hkv, B, max_q, keys, prefix_len, 0, bits, true, false).bytes);
 }
 
 sq_status run_attention(const void* q, int64_t q_stride, int64_t T, int hq,
@@ -1078,9 +1085,9 @@ sq_status run_attention(const void* q, int64_t q_stride, int64_t T, int hq,
   P.lse = lse;
   P.spin_limit = host::spin_limit();
   const int64_t keys = static_cast<int64_t>(width) * pages.page_size;
-  AttnPlan plan = make_plan(T, hq, pages.hkv, B, max_q, keys, prefix_len, pages.bits, true);
+  AttnPlan plan = make_plan(T, hq, pages.hkv, B, max_q, keys, prefix_len, rule.window, pages.bits, true);
   const bool have = ws && ws_bytes >= plan.bytes;
-  if (!have) plan = make_plan(T, hq, pages.hkv, B, max_q, keys, prefix_len, pages.bits, false);
+  if (!have) plan = make_plan(T, hq, pages.hkv, B, max_q, keys, prefix_len, rule.window, pages.bits, false);
   uint8_t* base = static_cast<uint8_t*>(ws);
   P.many_rows = plan.tile ? kFewRows : 0x7fffffff;
   P.few_rows = plan.stream ? kFewRows : 0;

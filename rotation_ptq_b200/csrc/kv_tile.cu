@@ -144,8 +144,20 @@ struct TileUnit {
 
 static_assert(sizeof(TileUnit) <= 128, "unit records");
 
-// Unit `x` of this launch; false if it is empty.
-__device__ __forceinline__ bool tile_unit(const AttnParams& P, int64_t x, TileUnit& u) {
+// First tile of the shared prefix that some new token sees (by a warp).
+__device__ __forceinline__ int first_shared_tile(const AttnParams& P) {
+  if (P.window == 0) return 0;
+  int least = 0x7fffffff;                  // position of the first new token of all
+  for (int b = threadIdx.x & 31; b < P.batch.B; b += 32) {
+    const Seq s = load_seq(P, b, false);
+    if (s.keys && s.qlen > 0) least = min(least, s.pos0);
+  }
+  least = __reduce_min_sync(0xffffffffu, least);
+  return min(max(least - P.window + 1, 0), P.prefix_len - 1) / KT;
+}
+
+// Unit `x` of this launch; false if it is empty.  low_tile: first_shared_tile().
+__device__ __forceinline__ bool tile_unit(const AttnParams& P, int64_t x, int low_tile, TileUnit& u) {
   const int G = P.G, hkv = P.pages.hkv, R = 2 * HALF;
   u.piece = static_cast<int>(x % P.nsplit);
   const int64_t y = x / P.nsplit;
@@ -162,8 +174,8 @@ __device__ __forceinline__ bool tile_unit(const AttnParams& P, int64_t x, TileUn
     u.pos0 = 0;
     u.len = 0;
     u.table = nullptr;
-    u.pt0 = 0;
-    u.pn = (P.prefix_len - 1) / KT + 1;
+    u.pt0 = low_tile;
+    u.pn = (P.prefix_len - 1) / KT + 1 - low_tile;
     u.ot0 = 0;
     const int per = (u.pn + P.nsplit - 1) / P.nsplit;
     u.first = min(u.pn, u.piece * per);
@@ -1190,12 +1202,13 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
       bool more = true;
       // no streaming kernel follows a call of one long sequence: its lengths are checked here
       if (P.few_rows == 0 && !P.shared && blockIdx.x == 0 && lane == 0) load_seq(P, 0, true);
+      const int low_tile = P.shared ? first_shared_tile(P) : 0;
       for (int k = 0; ok && more; ++k) {
         more = k * static_cast<int64_t>(gridDim.x) < units;
         const int64_t x = unit_index(k);
         TileUnit u;
         u.rows = 0;
-        if (more && (x >= units || !tile_unit(P, x, u))) continue;
+        if (more && (x >= units || !tile_unit(P, x, low_tile, u))) continue;
         ok = __all_sync(0xffffffffu, mbar_wait(&bar.u_free[at % UNITS], ((at / UNITS) & 1) ^ 1, spin));
         if (!ok) break;
         if (lane == 0) {

@@ -117,3 +117,25 @@ def test_scores_far_past_the_exponential(new, q_size, k_size, rule, bits):
         # weights (11 bits) and their sum's rounding, and bf16's
         slack = (2.0 ** -8 + 2.0 ** -9) * np.abs(seen).max()
         assert (o[i] <= seen.max(0) + slack).all() and (o[i] >= seen.min(0) - slack).all()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("window,in_a_pass", [(0, True), (100, False), (2500, True)])
+def test_prefix_under_a_window(window, in_a_pass, bits):
+    """A prefix is read once for the batch by what the window leaves of it: a short window's few keys are
+    streamed with each sequence's own, and a pass begins where the first token's window does - here that of a
+    sequence with fewer cached tokens than new ones."""
+    batch = 150
+    count = [1] * batch
+    own = [1 + b % 40 for b in range(batch)]
+    count[7], own[7] = 8, 2
+    prob = G.Attention(64, count, own, 8, 4, 32, bits, prefix=4000, window=window, pad=1)
+    need = sq.kv_attention_workspace_bytes(prob.T, 8, pages_of(prob.pool), batch, prob.table().shape[1], 8, 4000)
+    workspace = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    got = attend(prob, workspace=workspace)
+    check(prob, *got)
+    # the pass leaves its results behind what streaming alone uses
+    alone = sq.kv_attention_workspace_bytes(prob.T, 8, pages_of(prob.pool), batch, prob.table().shape[1], 8)
+    assert bool(workspace[alone:].any()) == in_a_pass
+    again = attend(prob, workspace=workspace)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
