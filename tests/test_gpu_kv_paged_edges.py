@@ -139,3 +139,137 @@ def test_prefix_under_a_window(window, in_a_pass, bits):
     assert bool(workspace[alone:].any()) == in_a_pass
     again = attend(prob, workspace=workspace)
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+def check_as_served(prob, out, lse):
+    """check(), with each row's bounds those of the kernel that serves its sequence: up to 32 rows (new tokens x
+    query heads per KV head) of a sequence are streamed, more go to the tile kernel, and so do all rows over a
+    prefix whose streaming tiles come to 30 an SM while no sequence has more than 128 rows."""
+    group, few = prob.hq // prob.hkv, 32
+    rows = max(prob.new) * group
+    per = 4 if rows <= 4 else 8 if rows <= 8 else 16
+    seen = min(prob.prefix, prob.rule["window"] + max(prob.new)) if prob.rule["window"] else prob.prefix
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    in_a_pass = len(prob.new) > 1 and prob.prefix and rows <= 128 and \
+        len(prob.new) * -(-rows // per) * prob.hkv * -(-seen // 128) >= 30 * sms
+    tile = np.repeat([bool(in_a_pass) or n * group > few for n in prob.new], prob.new)
+    ref = prob.reference()
+    wide, narrow = prob.bounds(ref, TILE_EPS, TILE_STEP), prob.bounds(ref, STREAM_EPS)
+    n = sum(prob.new)
+    b_out = np.where(tile[:, None, None], wide[0][:n], narrow[0][:n])
+    o, m = out.double().cpu().numpy()[:n], lse.double().cpu().numpy()[:n]
+    empty = np.isneginf(ref[1][:n])
+    assert np.array_equal(np.isneginf(m), empty) and (o[empty] == 0).all()
+    err = np.abs(o - ref[0][:n])
+    assert (err <= b_out).all(), "out: %.3g times its bound" % (err / b_out).max()
+    err = np.abs(m - np.where(empty, 0, ref[1][:n]))[~empty]
+    assert (err <= wide[1][:n][~empty]).all()
+    assert sq.device_status() == 0
+
+
+SERVED = [
+    dict(new=[5, 8, 1, 0], own=[300, 200, 90, 5], hq=16, hkv=4, page=16),               # 20 and 32 rows: streamed
+    dict(new=[1, 1], own=[333, 90], hq=16, hkv=1, page=16),
+    dict(new=[2, 1, 2], own=[700, 31, 40], hq=32, hkv=2, page=64),                      # 32 rows
+    dict(new=[1, 64, 2, 5, 0], own=[50, 64, 900, 5, 77], hq=8, hkv=2, page=32),         # both kernels in one call
+    dict(new=[1] * 7, own=[2, 4, 6, 16, 18, 64, 66], hq=32, hkv=8, page=32, prefix=130),        # a prefix in line
+    dict(new=[2, 5, 1], own=[2, 30, 200], hq=14, hkv=2, page=64, prefix=700),
+    dict(new=[1] * 160, own=[2 + 2 * (b % 30) for b in range(160)], hq=8, hkv=4, page=16, prefix=1000),     # in a pass
+]
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("kw", SERVED)
+def test_bounds_of_the_kernel_that_serves(kw, bits):
+    kw = dict(kw)
+    prob = G.Attention(65, kw.pop("new"), kw.pop("own"), bits=bits, pad=1, **kw)
+    check_as_served(prob, *attend(prob))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("kw", SERVED)
+def test_weights_keep_their_low_bits(kw, bits):
+    """Equal scores over values that all but cancel: + x (1 + 2^-12) and - x in turn.  The streaming kernel's 22
+    bits hold the difference, 2^-13 x of a row that sees pairs; 11 bits would lose all of it."""
+    kw = dict(kw)
+    prob = G.Attention(66, kw.pop("new"), kw.pop("own"), bits=bits, pad=1, **kw)
+    prob.q[:] = 0
+    x = 2.0 ** bits - 1
+    for b, n in enumerate(prob.own + [prob.prefix]):
+        pos = np.arange(n)
+        at = prob.pool.table[b, pos // prob.pool.page], slice(None), pos % prob.pool.page
+        odd = (pos & 1).astype(bool)
+        prob.pool.arrays["v_codes"][at] = np.where(odd, 0, 0xFF).astype(np.uint8)[:, None, None]
+        prob.pool.arrays["v_zero"][at] = np.where(odd, x, 0).astype(np.uint8)[:, None]
+        prob.pool.arrays["v_scale"][at] = np.where(odd, 1.0, 1 + 2.0 ** -12).astype(np.float32)[:, None]
+        value = np.where(odd, -x, x * (1 + 2.0 ** -12))
+        prob.values["v", b] = np.broadcast_to(value[:, None, None], (n, prob.hkv, 128)).copy()
+    check_as_served(prob, *attend(prob))
+
+
+@pytest.mark.parametrize("rule", [
+    dict(softcap=20.0), dict(softcap=0.5), dict(window=1), dict(window=33), dict(slopes=True),
+    dict(scale=0.31), dict(scale=-0.1), dict(scale=0.0), dict(softcap=30.0, window=70, slopes=True)])
+@pytest.mark.parametrize("prefix", [0, 45])
+def test_score_rules_8_bits(rule, prefix):
+    prob = G.Attention(67, [1, 4, 20], [150, 81, 20], 8, 2, 16, 8, prefix=prefix, pad=1, **rule)
+    check_as_served(prob, *attend(prob))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("rule", [{}, dict(softcap=20.0), dict(window=200, slopes=True)])
+@pytest.mark.parametrize("new,own,hq,hkv", [
+    ([1] * 64, [1 + (97 * b) % 1500 for b in range(64)], 48, 1),              # one 48-row token each
+    ([3 + b % 6 for b in range(40)], [9 + (61 * b) % 700 for b in range(40)], 16, 1),         # 48 to 128 rows
+    ([9 + 2 * b for b in range(24)], [70 + (131 * b) % 900 for b in range(24)], 8, 2),        # 36 to 220
+    ([5, 30], [4000, 900], 7, 1),                                             # few of them: split
+])
+def test_ragged_batches_of_tile_units(new, own, hq, hkv, rule, bits):
+    prob = G.Attention(68, new, own, hq, hkv, 32, bits, pad=1, **rule)
+    first = attend(prob)
+    check_as_served(prob, *first)
+    again = attend(prob)
+    n = sum(new)
+    assert torch.equal(first[0][:n], again[0][:n]) and torch.equal(first[1][:n], again[1][:n])
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("new", [1, 20])
+@pytest.mark.parametrize("rule", [{}, dict(window=60), dict(slopes=True)])
+def test_append_behind_a_prefix(new, rule, bits):
+    """Tokens appended behind a shared prefix, with rotary tables that begin at its length, are the tokens of a
+    sequence that holds the prefix's keys in pages of its own: the same codes, and the same attention."""
+    rng = np.random.default_rng(69)
+    hq, hkv, page, P, own = 8, 2, 16, 77, 41
+    N = P + own
+    x = bf16(G.round_bf16(rng.standard_normal((N, hq + 2 * hkv, 128))))
+    ang = np.arange(N)[:, None] * 1e4 ** (-np.arange(0, 128, 2) / 128)
+    cos, sin = cu(np.cos(ang).astype(np.float32)), cu(np.sin(ang).astype(np.float32))
+    slopes = cu((2.0 ** -np.arange(1, hq + 1)).astype(np.float32)) if rule.get("slopes") else None
+    args = dict(window=rule.get("window", 0), slopes=slopes)
+    i32 = lambda *a: cu(np.array(a, np.int32))  # noqa: E731
+    pages = sq.KVPages.empty(24, page, hkv, bits)
+    table = rng.permutation(24).astype(np.int32)
+    whole, shared, mine = cu(table[None, :8]), cu(table[8:13]), cu(table[None, 13:16])
+
+    def append(rows, table, tables):
+        t = x[rows]
+        return sq.kv_paged_append(t[:, :hq], t[:, hq:hq + hkv], t[:, hq + hkv:], pages, table, i32(0, t.shape[0]), i32(0),
+                                  *tables)
+
+    q = append(slice(0, N), whole, (cos, sin))[N - new:].contiguous()
+    append(slice(0, P), shared[None], (cos, sin))
+    q2 = append(slice(P, N), mine, (cos[P:].contiguous(), sin[P:].contiguous()))[own - new:].contiguous()
+    assert torch.equal(q, q2)
+    k, v = sq.kv_paged_dequant(pages, whole, i32(0, N), i32(0), N)
+    for got, want in zip(sq.kv_paged_dequant(pages, mine, i32(0, own), i32(0), own), (k, v)):
+        assert torch.equal(got, want[P:])
+    lse, lse2 = (torch.zeros((new, hq), device="cuda") for _ in range(2))
+    a = sq.kv_paged_attention(q, pages, whole, i32(0, new), i32(N), new, lse=lse, **args)
+    b = sq.kv_prefix_attention(q2, pages, shared, P, mine, i32(0, new), i32(own), new, lse=lse2, **args)
+    assert sq.device_status() == 0
+    # each is off by at most 2^-8 of itself and 2 (e + eps) of the largest value (see bounds() in tests/paged.py)
+    size = (q.double().abs().sum(-1).max() * k.double().abs().max() / 128 ** 0.5).item()
+    slack = 2 * (2.0 ** -18 * (1 + size) + TILE_EPS) * v.double().abs().max()
+    assert ((a.double() - b.double()).abs() <= 2 * (2.0 ** -8 * torch.maximum(a, b).double().abs() + slack)).all()
+    assert ((lse - lse2).abs() <= 2 * 2.0 ** -18 * (1 + size)).all()
