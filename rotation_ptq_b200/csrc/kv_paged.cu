@@ -98,7 +98,7 @@ __device__ __forceinline__ void across(R (&y)[16], int s, unsigned mask) {
 template <class R, bool WHOLE>
 __device__ __forceinline__ R scale_and_turn(const uint4 (&raw)[2], const __nv_bfloat16* src, const float* w,
                                             const Factors& fac, const float* cs, const float* sn,
-                                            int rot, bool interleaved, int s, R (&y)[16]) {
+                                            int rot, bool interleaved, int s, R (&y)[16], float scale = 1.0f) {
   R sum = 0;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
@@ -149,7 +149,7 @@ __device__ __forceinline__ R scale_and_turn(const uint4 (&raw)[2], const __nv_bf
       if (w) floats8(w + p0, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        R t = b[e];
+        R t = sizeof(R) == 4 ? b[e] * scale : b[e];        // (the lane's own values have it already)
         if (w) t *= static_cast<R>(g[e]);
         t *= static_cast<R>(ss[e]);
         y[8 * c + e] = y[8 * c + e] * static_cast<R>(cc[e]) + (upper ? t : -t);
@@ -158,6 +158,10 @@ __device__ __forceinline__ R scale_and_turn(const uint4 (&raw)[2], const __nv_bf
   }
   return sum;
 }
+
+// A query whose squares float32 does not hold (values past 1e18, or all below 1e-15 with an eps as small) is
+// taken again by this or its reciprocal: the norm does not depend on it.
+constexpr float kUp = 1.2089258e24f;       // 2^80
 
 // f H, f = rsqrt(mean x^2 + eps) / sqrt(128) (w) or 1 / sqrt(128): in double.
 __device__ __forceinline__ void finish(double (&y)[16], double sum, bool norm, float eps, int s, unsigned mask) {
@@ -183,13 +187,20 @@ __device__ __forceinline__ void finish(double (&y)[16], double sum, bool norm, f
   for (int e = 0; e < 16; ++e) y[e] *= f;
 }
 
-// The same in float32, two values (the lane's two chunks) an instruction.
-__device__ __forceinline__ void finish(float (&y)[16], float sum, bool norm, float eps, int s, unsigned mask) {
+// The same in float32, two values (the lane's two chunks) an instruction, of a vector of `scale` times its
+// values.  False where its mean square leaves float32: then `scale` is the power of two to take it by.
+__device__ __forceinline__ bool finish(float (&y)[16], float sum, bool norm, float eps, int s, unsigned mask,
+                                       float& scale) {
   float f = 0.088388347648318440550f;
   if (norm) {
 #pragma unroll
     for (int o = 1; o < LPV; o <<= 1) sum += __shfl_xor_sync(mask, sum, o);
-    f *= 1.0f / sqrtf(sum * (1.0f / D) + eps);
+    const float mean = sum * (1.0f / D) + eps * scale * scale;
+    if (scale == 1.0f && !(mean >= 1e-30f && mean <= 1e34f)) {
+      scale = mean < 1.0f ? kUp : 1.0f / kUp;
+      return false;
+    }
+    f *= 1.0f / sqrtf(mean);
   }
   f2 v[8];
 #pragma unroll
@@ -215,6 +226,7 @@ __device__ __forceinline__ void finish(float (&y)[16], float sum, bool norm, flo
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) y[e] = v[e].x, y[8 + e] = v[e].y;
+  return true;
 }
 
 // Quantizes one vector held by 8 lanes (lane s: chunks s and s + 8) into row
@@ -306,9 +318,20 @@ __global__ void __launch_bounds__(256, 3) append_kernel(const AppendParams P) {
       }
       if (job < P.jq) {
         const int head = job * VPW + vec;
-        float y[16];
-        const float sum = scale_and_turn<float, WHOLE>(mine, now, P.q_norm, fac, cs, sn, P.rot, P.interleaved, s, y);
-        finish(y, sum, P.q_norm != nullptr, P.eps, s, mask);
+        float y[16], scale = 1.0f;
+        uint4 in[2] = {mine[0], mine[1]};
+#pragma unroll 1
+        for (;;) {
+          const float sum = scale_and_turn<float, WHOLE>(in, now, P.q_norm, fac, cs, sn, P.rot, P.interleaved, s, y, scale);
+          if (finish(y, sum, P.q_norm != nullptr, P.eps, s, mask, scale)) break;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            in[c] = *reinterpret_cast<const uint4*>(now + 64 * c + 8 * s);
+            __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&in[c]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], __float2bfloat162_rn(scale));
+          }
+        }
         if (head < P.hq) {
           __nv_bfloat16* dst = P.q_out + (t * P.hq + head) * D + 8 * s;
 #pragma unroll
