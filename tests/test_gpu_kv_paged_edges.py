@@ -273,3 +273,63 @@ def test_append_behind_a_prefix(new, rule, bits):
     slack = 2 * (2.0 ** -18 * (1 + size) + TILE_EPS) * v.double().abs().max()
     assert ((a.double() - b.double()).abs() <= 2 * (2.0 ** -8 * torch.maximum(a, b).double().abs() + slack)).all()
     assert ((lse - lse2).abs() <= 2 * 2.0 ** -18 * (1 + size)).all()
+
+
+@pytest.mark.parametrize("size", [1e-38, 1e-30, 1e-20, 1e20, 1e30, 1e36])
+@pytest.mark.parametrize("kind", ["split", "whole", "pass"])
+def test_value_scales_at_the_ends_in_pieces(kind, size):
+    """As partial results that are joined, as whole units, and over a prefix that is read once."""
+    if kind == "pass":
+        prob = G.Attention(71, [1] * 160, [1 + b % 30 for b in range(160)], 8, 4, 16, 4, prefix=1000, v_size=size)
+    else:
+        prob = G.Attention(71, [64, 40], [1500, 700], 4, 1, 16, 4, v_size=size)
+    ws = torch.zeros(16, dtype=torch.uint8, device="cuda") if kind == "whole" else None
+    check(prob, *attend(prob, workspace=ws))
+
+
+@pytest.mark.parametrize("factor", [1e9, 1e20, 1e30])
+@pytest.mark.parametrize("kind", ["split", "whole", "pass"])
+def test_hidden_value_scales_in_pieces(kind, factor):
+    """The same for keys with large scales that only some rows see, first by the window and then no more."""
+    if kind == "pass":
+        prob = G.Attention(72, [1] * 160, [1 + b % 40 for b in range(160)], 8, 4, 16, 4, prefix=1200, window=1000)
+        pos, b = 215, 160                          # position 215 is visible up to 1214: to own lengths up to 15
+    else:
+        prob = G.Attention(72, [64], [1500], 4, 1, 16, 4, window=1000)
+        pos, b = 470, 0                            # visible up to 1469
+    ref = prob.reference()
+    b_out, b_lse = prob.bounds(ref, TILE_EPS, TILE_STEP)
+    page = prob.pool.table[b, pos // 16]
+    prob.pool.arrays["v_scale"][page, :, pos % 16] *= np.float32(factor)
+    ws = torch.zeros(16, dtype=torch.uint8, device="cuda") if kind == "whole" else None
+    out, lse = attend(prob, workspace=ws)
+    at = np.concatenate([prob.prefix + own - n + np.arange(n) for n, own in zip(prob.new, prob.own)])
+    blind = at - pos >= 1000
+    assert blind.any() and not blind.all()
+    o, m = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    err = np.abs(o - ref[0])[blind] / b_out[blind]
+    assert (err <= 1).all(), "out: %.3g times its bound" % err.max()
+    assert (np.abs(m - ref[1]) <= b_lse).all() and np.isfinite(o).all()
+    assert sq.device_status() == 0
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("kw", [
+    dict(new=[1], own=[90]), dict(new=[6], own=[80]), dict(new=[64], own=[300]), dict(new=[64], own=[300], softcap=20.0),
+    dict(new=[1] * 160, own=[1 + b % 30 for b in range(160)], hq=8, hkv=4, prefix=1000)])
+def test_a_query_that_is_not_finite_keeps_to_its_row(kw, bad):
+    kw = dict(dict(hq=4, hkv=1), **kw)
+    prob = G.Attention(73, kw.pop("new"), kw.pop("own"), bits=4, **kw)
+    ref = prob.reference()
+    b_out, b_lse = prob.bounds(ref, TILE_EPS, TILE_STEP)
+    q = bf16(prob.q)
+    row, head = prob.T // 2, 1
+    q[row, head, 5] = bad
+    out, lse = attend(prob, q=q)
+    o, m = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    others = np.ones((prob.T, prob.hq), bool)
+    others[row, head] = False
+    assert (np.abs(o - ref[0]) <= b_out)[others].all() and (np.abs(m - ref[1]) <= b_lse)[others].all()
+    if not prob.rule["softcap"]:                   # (a cap makes an infinite score a finite one)
+        assert np.isnan(o[row, head]).any()
+    assert sq.device_status() == 0
