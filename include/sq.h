@@ -634,9 +634,10 @@ typedef struct {
  * float32; the output is rounded once to bf16.  A row with no visible key (p < 0) gets
  * zeros and lse -inf.  Weights of the softmax are held to 22 bits for sequences
  * of up to 32 rows (new tokens x hq / hkv), to 11 bits (fp16) for more and over a
- * prefix that is read once for the batch; times their values' scales they are
- * held in steps no coarser than 2^-37 and 2^-32 of the row's largest weight times
- * the largest scale that it sees.
+ * prefix that is read once for the batch (so a sequence's result may differ, by an
+ * eighth of its own rounding, with the sizes of the whole call).  Times their
+ * values' scales they are held in steps no coarser than 2^-37 and 2^-32 of the
+ * row's largest weight times the largest scale that it sees.
  *
  * q          device bf16 [T][hq][d] (q_out of the append), heads contiguous,
  *            q_stride elements between tokens (a multiple of 8).  Any finite

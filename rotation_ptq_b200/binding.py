@@ -836,9 +836,12 @@ def kv_paged_attention(q: torch.Tensor, pages: KVPages, block_table: torch.Tenso
     (0: none has any, and nothing is written).
     scale defaults to 1/sqrt(128); softcap caps scores by a tanh; window hides
     keys that far back; slopes (float32 [hq]) subtract slope x distance.
-    Returns bf16 [T, hq, 128]; lse (float32 [T, hq]), where given, is written.
+    Returns bf16 [T, hq, 128]; lse (float32 [T, hq]), where given, is written;
+    rows behind cu_seqlens[B] are not.  The softmax's weights are held to 22 bits
+    for sequences of up to 32 rows (new tokens x query heads per KV head), to 11
+    for more, an eighth of what the bf16 result's own rounding may lose.
     Without ``workspace`` a cached buffer of the stream is used; under stream
-    capture, one that belongs to the graph.
+    capture, one that belongs to the graph.  Host threads may call on one stream.
     """
     return _kv_attention(q, pages, None, 0, block_table, cu_seqlens, lengths, max_q, scale,
                          softcap, window, slopes, out, lse, workspace)
@@ -853,7 +856,9 @@ def kv_prefix_attention(q: torch.Tensor, pages: KVPages, prefix_table: torch.Ten
     """kv_paged_attention behind a shared prefix (``sq_kv_prefix_attention``):
     the first prefix_len positions of every sequence are the rows of the pages
     prefix_table (int32 [pages]); lengths counts each sequence's own rows
-    behind them.  The prefix is read once for the batch where that pays.
+    behind them.  The prefix is read once for the batch where that pays, its
+    weights then held to 11 bits: which it is goes by the call's sizes, so a
+    sequence's result may differ by that with the others of its batch.
     """
     if not isinstance(prefix_table, torch.Tensor) or prefix_table.dim() != 1:
         raise ValueError("prefix_table must be int32 [pages]")

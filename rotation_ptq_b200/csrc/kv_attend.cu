@@ -18,13 +18,17 @@
 // over a long cache of codes that are all positive would lose, against one of
 // both signs, what its mean is larger than the result.
 //
-// What bounds it: issue slots, and the beginning and end of a unit (about 3 us
-// from its first load to its first key and 4 from its last key to the end of
-// its pieces' join).  16 keys x 128 channels take a warp 363 instructions
-// (592 with codes widened to whole numbers and loads straight to registers);
-// two documents of 118 to 131 thousand keys, 280 MB: 85 us (158), of which the
-// keys 60, at 4.7 TB/s.  Loads go through a ring of two slots of 32 keys in
-// shared memory per warp (cp.async, no exchange between warps).
+// What bounds it: issue slots, and the beginning and end of a unit.  Stamps of
+// a copy, us from the launch: one sequence of 577 keys, first key 3.6, the last
+// CTA's last key 3.9, end 10.7; 16 x 4096, 4.5, 25.8 and 32.0; 48 ragged, 8
+// bits, capped, 8.2, 60.7 and 69.0; two of 118 to 131 thousand, 6.1, 74.4 and
+// 84.3 (from a last key to its piece's arrival 3, the rest is the join of
+// pieces).  16 keys x 128 channels take a warp 392 instructions, a unit's ends
+// shared out (374 before rows had normalisers of their own; 592
+// with codes widened to whole numbers and loads straight to registers); those two
+// documents, 280 MB, take 85 us (158), of which the keys 60, at 4.7 TB/s.
+// Loads go through a ring of two slots of 32 keys in shared memory per warp
+// (cp.async, no exchange between warps).
 //
 // Exactness: queries are scaled per row by a power of two that puts the
 // largest at 2^14..2^15 and held in fp16 (a bf16 value has 8 significant

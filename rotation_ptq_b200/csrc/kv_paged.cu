@@ -18,12 +18,13 @@
 // token's place once, while the first heads' values are already on their way,
 // and always has the next heads' loads in flight.
 //
-// What bounds it: issue slots (69 %) and the shuffles of the cross-lane stages;
-// 16,384 tokens of 32 + 2 x 8 heads at 4 bits take 113 us (354 MB, 54 us of
-// HBM) and their read-back 22 (85 MB, 13; bound by the chain from a token to its
-// rows), both together 270 with a warp per job that looked its token up again
-// and waited for its loads.  Registers for 3 CTAs an SM: 2 take 120 us, 4
-// (spills) 138.
+// What bounds it: issue slots (70 %) and the shuffles of the cross-lane stages;
+// 16,384 tokens of 32 + 2 x 8 heads at 4 bits take 114 us (354 MB, 54 us of
+// HBM; 112 before queries of any size were taken) and their read-back 23 right
+// behind it, 29 from cold caches (85 MB, 13; bound by the chain from a token to
+// its rows), both together 270 with a warp per job that looked its token up again
+// and waited for its loads.  Registers for 3 CTAs an SM: of an earlier form that
+// took 113 us, 2 took 120, 4 (spills) 138.
 //
 // Q is computed in float32 (its output is bf16).  K is computed in double
 // precision and rounded once to float32, so its codes are those of the exact

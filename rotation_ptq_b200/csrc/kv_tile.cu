@@ -25,7 +25,9 @@
 // lane reads them all: those broadcasts and the products' operand reads, both
 // from shared memory, slow one another 1.5 times); caps and slopes compiled by
 // themselves, 546 to 449 (the softmax's loop is a third shorter; more copies of
-// its parts for special cases cost more than their branches: 510).  What bounds
+// its parts for special cases cost more than their branches: 510).  Rows' own
+// value scales in their references took it to 464 and scores of any size to 469:
+// it is the code that counts, more than the times it runs.  What bounds
 // it is the softmax's own latency: when the whole took 541 us, it took 275
 // without its arithmetic, 460 without the products, 446 without the widening and
 // as long as before without the exponentials alone.
