@@ -25,9 +25,11 @@
 // lane reads them all: those broadcasts and the products' operand reads, both
 // from shared memory, slow one another 1.5 times); caps and slopes compiled by
 // themselves, 546 to 449 (the softmax's loop is a third shorter; more copies of
-// its parts for special cases cost more than their branches: 510).  Rows' own
-// value scales in their references took it to 464 and scores of any size to 469:
-// it is the code that counts, more than the times it runs.  What bounds
+// its parts for special cases cost more than their branches: 510).  It is the
+// code that counts, more than the times it runs: rows' own value scales in their
+// references and scores of any size, all in a branch that few steps take, cost
+// 449 to 473, and one copy of the issuing code for both halves instead of two
+// gave 438.  What bounds
 // it is the softmax's own latency: when the whole took 541 us, it took 275
 // without its arithmetic, 460 without the products, 446 without the widening and
 // as long as before without the exponentials alone.
@@ -73,8 +75,8 @@ constexpr uint32_t IDESC_S = idesc_f16(128, KT / 2, false, false);
 // most of a prompt's steps).  fp16 then holds weights in full down to 2^-(14 + kTop) of the largest and in
 // fixed steps of 2^-(24 + kTop) below.  A row's own scales count, since a hidden key's, however large, has
 // no business with its weights' precision; where a step shows a row a part of its keys, the exponent
-// is looked up by the run that it sees (prompts 464 us, against 452 with one exponent for all of a warp's
-// rows; 600 taken off the scores' registers, 530 in a loop over the keys).
+// is looked up by the run that it sees (prompts, when this came, 464 us, against 452 with one exponent for
+// all of a warp's rows; 600 taken off the scores' registers, 530 in a loop over the keys).
 constexpr float kTop = 10.0f, kSlack = 5.0f;
 // Value scales are taken as they are while a step's largest is within 2^+-kEnds, else times a power of two
 // for all rows of the warp.  A row whose own are up to 2^kReach below that keeps its precision.
@@ -427,10 +429,9 @@ __device__ __forceinline__ void widen_rows(uint8_t* dst, const TileCodes<BITS>& 
 }
 
 // The products of half H, by one warp.  Tensor memory is the whole SM's (512 columns), so its address is 0.
-template <int H>
-__device__ __forceinline__ void issue_products(const AttnParams& P, uint8_t* smem, TileBars& bar,
+__device__ __forceinline__ void issue_products(int H, const AttnParams& P, uint8_t* smem, TileBars& bar,
                                                const TileUnit* ring_u) {
-  constexpr uint32_t t_s = H * 128, t_o = 256 + H * 128;
+  const uint32_t t_s = H * 128, t_o = 256 + H * 128;
   const uint32_t spin = P.spin_limit, elected = elect_lane();
   bool ok = true;
   int tiles = 0;
@@ -1192,11 +1193,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
     // ------------------------------------------------------------ products
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(BITS == 4 ? 64 : 56));
     // one warp per half, which sleeps while its half has nothing to do: a single one that polls both
-    // halves' barriers takes issue slots and shared memory from the warps that work
-    if (warp == 12) {
-      issue_products<0>(P, smem, bar, ring_u);
-    } else if (warp == 13) {
-      issue_products<1>(P, smem, bar, ring_u);
+    // halves' barriers takes issue slots and shared memory from the warps that work.  One copy of its code
+    // serves both (with the half a constant of two copies, prompts took 477 us against 438)
+    if (warp <= 13) {
+      issue_products(warp - 12, P, smem, bar, ring_u);
     } else if (warp == 14) {
       // ------------------------------------------------------------- units
       const int64_t units = P.units;
