@@ -28,7 +28,7 @@
 // its parts for special cases cost more than their branches: 510).  It is the
 // code that counts, more than the times it runs: rows' own value scales in their
 // references and scores of any size, all in a branch that few steps take, cost
-// 449 to 473, and one copy of the issuing code for both halves instead of two
+// 449 to 477, and one copy of the issuing code for both halves instead of two
 // gave 438.  What bounds
 // it is the softmax's own latency: when the whole took 541 us, it took 275
 // without its arithmetic, 460 without the products, 446 without the widening and
