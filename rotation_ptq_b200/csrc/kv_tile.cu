@@ -78,9 +78,10 @@ constexpr uint32_t IDESC_S = idesc_f16(128, KT / 2, false, false);
 // is looked up by the run that it sees (prompts, when this came, 464 us, against 452 with one exponent for
 // all of a warp's rows; 600 taken off the scores' registers, 530 in a loop over the keys).
 constexpr float kTop = 10.0f, kSlack = 5.0f;
-// Value scales are taken as they are while a step's largest is within 2^+-kEnds, else times a power of two
-// for all rows of the warp.  A row whose own are up to 2^kReach below that keeps its precision.
-constexpr float kEnds = 60.0f, kReach = 100.0f;
+// Value scales are taken as they are while a step's largest is within 2^+-kEnds, else times a power of two,
+// for all rows of the warp, that brings it to 2^+-kInside.  A row whose own are 2^-kReach and more of
+// what they are then keeps its precision: beside hidden ones near float32's end, those from 2^-12 on.
+constexpr float kEnds = 60.0f, kInside = 40.0f, kReach = 100.0f;
 // The sums of exponentials are held at 2^-40 of themselves: beside large scales, exponentials are up to
 // 2^(kTop + kSlack + kReach).
 constexpr float kDown = 9.094947e-13f;
@@ -780,7 +781,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
             float seen = sve + sv_exp, shift = 0.f, low = 0.f;
             if (sve > kEnds) {
               // the scales' factor moves, and references with it as far as the sums of exponentials allow
-              const float to = fabsf(seen) > kEnds ? fminf(seen, 126.f) : 0.f;
+              const float to = seen > kEnds ? seen - kInside : seen < -kEnds ? seen + kInside : 0.f;
               shift = to - sv_exp;
               sv_exp = to;
               const float most = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));

@@ -61,7 +61,7 @@ def scale_key(prob, pos, factor):
 
 
 @pytest.mark.parametrize("bits", [4, 8])
-@pytest.mark.parametrize("factor", [1e9, 1e20, 1e30])
+@pytest.mark.parametrize("factor", [1e9, 1e20, 1e30, 1e38])
 @pytest.mark.parametrize("new,own,window,pos", [
     (6, 80, 0, 79),                                 # streaming kernel: a later token's key
     (6, 80, 10, 65),                                # one that only the first token still sees
@@ -287,7 +287,7 @@ def test_value_scales_at_the_ends_in_pieces(kind, size):
     check(prob, *attend(prob, workspace=ws))
 
 
-@pytest.mark.parametrize("factor", [1e9, 1e20, 1e30])
+@pytest.mark.parametrize("factor", [1e9, 1e20, 1e30, 1e38])
 @pytest.mark.parametrize("kind", ["split", "whole", "pass"])
 def test_hidden_value_scales_in_pieces(kind, factor):
     """The same for keys with large scales that only some rows see, first by the window and then no more."""
