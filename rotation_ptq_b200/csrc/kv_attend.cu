@@ -169,7 +169,7 @@ struct Stream {
       float f = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
       const float inv = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
       // a factor >= 0 lets the maximum be taken before it is applied
-      float mine = inv * P.scale * (P.cap > 0.f ? 1.0f / P.cap : kLog2e);
+      float mine = inv * P.scale * (P.cap > 0.f ? 1.0f : kLog2e);
       if (mine < 0.f) mine = -mine, f = -f;
       if (mine == 0.f) mine = 1.f, f = 0.f;
       mine = fminf(mine, 3.0e38f);         // times a score of zero, an infinity would be NaN
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(THREADS, Stream<BITS, NT, PAIR>::CTAS) stream_
                   float x = sc[gr][n][e];
                   const int dist = qpos[n][c] - (kpos + 16 * gr + g + 8 * hf);
                   if (special) {
-                    if (P.cap > 0.f) x = P.cap * kLog2e * tanh_score(x);
+                    if (P.cap > 0.f) x = P.cap * tanh_score(x * P.inv_cap) * kLog2e;
                     x = fmaf(-slope[n][c], static_cast<float>(dist), x);
                   }
                   const bool seen = dist >= 0 && (P.window == 0 || dist < P.window) &&
@@ -1083,6 +1083,7 @@ sq_status run_attention(const void* q, int64_t q_stride, int64_t T, int hq,
   P.G = hq / pages.hkv;
   P.scale = rule.scale;
   P.cap = rule.softcap;
+  P.inv_cap = rule.softcap > 0.f ? std::min(1.0f / rule.softcap, 3.0e38f) : 0.f;
   P.window = rule.window;
   P.slopes = rule.slopes;
   P.out = static_cast<__nv_bfloat16*>(out);

@@ -46,6 +46,7 @@ struct AttnParams {
   int ex_n;                                // pieces, 0: none
   float* ex_o;                             // [piece][T][hq][128]
   float* ex_ml;                            // [piece][T][hq][2]
+  float inv_cap;                           // 1 / cap, at most 3e38: in the queries' factors a large cap leaves float32
 };
 
 // One sequence's new tokens and keys.  Positions count the shared prefix

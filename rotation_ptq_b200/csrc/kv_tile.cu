@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
           const int up = mx > 0.f ? max(-126, min(126, 14 - ex)) : 0;
           float qf = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
           float f = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * P.scale *
-                    (P.cap > 0.f ? 1.0f / P.cap : kLog2e);
+                    (SPECIAL && P.cap > 0.f ? 1.0f : kLog2e);
           // a factor >= 0 lets the maximum be taken before it is applied
           if (f < 0.f) f = -f, qf = -qf;
           if (f == 0.f) f = 1.f, qf = 0.f;
@@ -704,8 +704,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_kernel(const AttnParams 
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                   w[bk][e] = __float_as_uint(
-                      P.cap * kLog2e *
-                      tanh_score(__uint_as_float(w[bk][e]) * ((e & 1) ? sk.y : sk.x) * f[2 * bk + (e >> 1)]));
+                      P.cap * tanh_score(__uint_as_float(w[bk][e]) * ((e & 1) ? sk.y : sk.x) *
+                                         f[2 * bk + (e >> 1)] * P.inv_cap) * kLog2e);
                 tmem_st_16x256b_x1(t_s + (bk << 20) + 8 * c, w[bk]);
               }
             }

@@ -333,3 +333,26 @@ def test_a_query_that_is_not_finite_keeps_to_its_row(kw, bad):
     if not prob.rule["softcap"]:                   # (a cap makes an infinite score a finite one)
         assert np.isnan(o[row, head]).any()
     assert sq.device_status() == 0
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("cap", [1e9, 1e25, 1e33, 2.9e38])
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("new", [1, 5, 64])
+def test_a_large_cap_is_none(new, slopes, cap, bits):
+    """Scores a billion times below their cap are the scores to float32's accuracy (x - x^3 / 3 at x = 1e-8)."""
+    prob = G.Attention(74, [new], [150], 4, 1, 16, bits, slopes=slopes)
+    check(prob, *attend(prob, softcap=cap))
+
+
+@pytest.mark.parametrize("new", [1, 64])
+@pytest.mark.parametrize("cap", [1e-3, 1e-20, 1e-44])
+def test_a_small_cap_leaves_equal_weights(new, cap):
+    """Scores of at most 1e-3 apart from zero: the weights of a row are equal to that."""
+    prob = G.Attention(75, [new], [150], 4, 1, 16, 4)
+    out, lse = attend(prob, softcap=cap)
+    prob.rule["scale"] = 0.0
+    ref = prob.reference()
+    b_out, b_lse = prob.bounds(ref, TILE_EPS + 2 * cap, TILE_STEP)
+    o, m = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert (np.abs(o - ref[0]) <= b_out).all() and (np.abs(m - ref[1]) <= b_lse + cap).all()
