@@ -984,14 +984,21 @@ int stream_grid(int bits, int kind) {
 // Sequences of up to this many rows (new tokens x query heads per KV head) go to the streaming kernel
 // (in units of 16), longer ones to the tile kernel, whose 128 rows a half cost the same however few of
 // them live.  4-bit, 4000 keys, streaming against tile, us: 32 rows of 1, 4, 16 sequences 29 / 28,
-// 36 / 44, 85 / 103; 48 rows 30 / 34, 52 / 46, 122 / 102.
+// 36 / 44, 85 / 103; 48 rows 30 / 34, 52 / 46, 122 / 102.  With 4 KV heads instead of 8, 1, 4, 16, 48 sequences
+// at 4 bits, 32 rows 33 / 27, 30 / 35, 54 / 59, 130 / 184 (8 bits 33 / 28, 30 / 34, 56 / 69, 130 / 223), 64 rows
+// 29 / 34, 37 / 41, 89 / 86, 228 / 182 (8 bits 29 / 35, 38 / 39, 91 / 107, 226 / 223), 128 rows 29 / 50, 54 / 48,
+// 158 / 87, 423 / 183.  Where there are few units streaming would still win above kFewRows, 48 rows of a single
+// KV head at all of these (31 / 34, 28 / 38, 35 / 40, 55 / 58): the tile kernel's work is cut by places, not keys.
 constexpr int kFewRows = 32;
 // A shared prefix is read once for the batch (by the tile kernel, whose partial results the streaming
 // kernel joins) while no sequence has more rows than kSharedRows - longer ones fill the tile kernel's
 // rows by themselves - and the streaming kernel's tiles over the prefix, for each sequence anew, would
 // come to kSharedTiles an SM.  4-bit, us, streaming against shared: 16 single tokens behind 4096 keys
 // 38 / 42, behind 10000 67 / 52; 32 behind 2000 42 / 43, behind 4096 60 / 44; 64 behind 700 44 / 55,
-// behind 2000 65 / 55; 5 new tokens each, 6 sequences behind 2000 39 / 47, 32 behind 2000 108 / 89.
+// behind 2000 65 / 55; 5 new tokens each, 6 sequences behind 2000 39 / 47, 32 behind 2000 108 / 89.  8-bit:
+// 16 single tokens behind 4096 39 / 39, behind 10000 68 / 45; 32 behind 2000 44 / 37, behind 4096 60 / 43; 64 behind
+// 700 43 / 51, behind 2000 65 / 54; 6 behind 10000 35 / 43; 5 new tokens each, 6 behind 4096 56 / 53, behind 10000
+// 97 / 58, 16 behind 2000 64 / 50, 32 behind 700 84 / 73: where the rule is wrong, it is by a quarter at most.
 // Under a window only the prefix's last keys count: either side reads no others.
 constexpr int kSharedRows = 128;
 constexpr int kSharedTiles = 30;
