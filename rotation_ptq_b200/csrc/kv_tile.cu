@@ -29,7 +29,7 @@
 // code that counts, more than the times it runs: rows' own value scales in their
 // references and scores of any size, all in a branch that few steps take, cost
 // 449 to 477, and one copy of the issuing code for both halves instead of two
-// gave 438.  What bounds
+// gave 438 (445 with what caps of any size changed around it).  What bounds
 // it is the softmax's own latency: when the whole took 541 us, it took 275
 // without its arithmetic, 460 without the products, 446 without the widening and
 // as long as before without the exponentials alone.
